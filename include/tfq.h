@@ -79,8 +79,9 @@ typedef enum tfq_status {
     TFQ_ETIMEOUT = 4       /* a bounded device-side wait ran out             */
 } tfq_status;
 
-/* Output element type of the per-row weight quantizer. */
-enum { TFQ_DTYPE_FP8_E4M3 = 0, TFQ_DTYPE_INT8 = 1 };
+/* Element types: the output of the per-row weight quantizer (the first two),
+ * the operands of the layer norm and the rotary positions (the others). */
+enum { TFQ_DTYPE_FP8_E4M3 = 0, TFQ_DTYPE_INT8 = 1, TFQ_DTYPE_BF16 = 2, TFQ_DTYPE_FP16 = 3, TFQ_DTYPE_FP32 = 4 };
 
 /* Largest K (row length) the row quantizers accept (keeps the kernels' index
  * arithmetic in 32 bits).  Larger K returns TFQ_EUNSUPPORTED. */
@@ -303,6 +304,167 @@ TFQ_API tfq_status tfq_mxfp8_linear(const void *A_q, const void *sf_a, const voi
                                     void *stream);
 
 /*
+ * ------------------------------------------------------------------------
+ * Around the Linear of a transformer block: the norm in front of it, low-rank
+ * adapters beside it, rotary positions on the queries and keys behind it.
+ * (Additions of this library; the pages name the Linear only.)  In these
+ * entry points x, dy, q, k and what has their type may be strided and need
+ * only their own element's alignment where so stated: 16-byte accesses are
+ * used where every row allows them, element accesses otherwise.
+ * ------------------------------------------------------------------------
+ *
+ * tfq_layer_norm: for row m of group g = m / (M / groups),
+ *   mean[m] = 1/K sum_k x[m,k],  rstd[m] = 1 / sqrt(1/K sum_k (x[m,k] - mean[m])^2 + eps),
+ *   y[m,k]  = (x[m,k] - mean[m]) rstd[m] (weight[g,k] + weight_offset) + bias[g,k].
+ * groups == 1 is the ordinary norm; groups > 1 gives every M / groups
+ * consecutive rows a weight and bias of their own (the adaptive norm of a
+ * diffusion transformer: weight = scale, weight_offset = 1, bias = shift).
+ *   x      : [M, K] of `dtype` (TFQ_DTYPE_BF16, _FP16 or _FP32), rows x_stride
+ *            elements apart (x_stride >= K); element-aligned.
+ *   weight, bias : [groups, K] dense, of `w_dtype` (dtype or TFQ_DTYPE_FP32),
+ *            or NULL (a missing weight multiplies by 1 whatever weight_offset is,
+ *            a missing bias is 0); element-aligned.
+ *   y      : [M, K] dense, of `dtype`, written.
+ *   mean, rstd : [M] fp32, written, or both NULL.
+ * Statistics are fp32; the variance is summed from x - mean.  NaN or inf in a
+ * row makes that row of y NaN (or inf) and no other.  eps == 0 is allowed (a
+ * constant row is then NaN).
+ * M == 0 or K == 0 is a no-op.
+ * Errors: TFQ_EINVAL (negative sizes, unknown types, groups < 1, M % groups != 0,
+ * x_stride < K, eps negative or not finite, weight_offset not finite, a null or
+ * not element-aligned pointer, one of mean and rstd without the other),
+ * TFQ_EUNSUPPORTED (K > TFQ_NORM_MAX_K, M >= 2^31, groups * K >= 2^31, not sm_100).
+ */
+#define TFQ_NORM_MAX_K 32768
+TFQ_API tfq_status tfq_layer_norm(const void *x, int64_t x_stride, int dtype, const void *weight, const void *bias,
+                                  int w_dtype, float weight_offset, int64_t M, int64_t K, int64_t groups, float eps,
+                                  void *y, float *mean, float *rstd, void *stream);
+
+/*
+ * tfq_layer_norm_quant_fp8: the norm above straight to the W8A8 Linear's
+ * input: with y the fp32 value of the formula above (not rounded to `dtype`),
+ *   s[m] = fl32(max(max_k |y[m,k]|, 1e-12f) / qmax),  q[m,k] = cast_E4M3FN(clamp(y[m,k] / s[m], -qmax, qmax)).
+ *   q_e4m3 : [M, K] bytes, s : [M] fp32, 16-byte aligned, written.
+ * The codes are those of the fp32 norm, so they can differ in the last place
+ * from tfq_quant_act_fp8_per_token's on a bf16 norm output, which carries one
+ * rounding more.
+ * M == 0 is a no-op; K == 0 writes s only.
+ * Errors as tfq_layer_norm, and TFQ_EINVAL for K % 16 != 0, qmax outside
+ * [1, 448] or an output that is not 16-byte aligned.
+ */
+TFQ_API tfq_status tfq_layer_norm_quant_fp8(const void *x, int64_t x_stride, int dtype, const void *weight,
+                                            const void *bias, int w_dtype, float weight_offset, int64_t M, int64_t K,
+                                            int64_t groups, float eps, float qmax, void *q_e4m3, float *s,
+                                            void *stream);
+
+/*
+ * tfq_layer_norm_backward: the gradients of tfq_layer_norm.  With
+ * xhat = (x - mean) rstd and h = dy (weight[g] + weight_offset):
+ *   dx[m,k]      = rstd[m] (h - 1/K sum_k h - xhat 1/K sum_k h xhat)
+ *   dweight[g,k] = sum over the rows m of group g of dy[m,k] xhat[m,k]
+ *   dbias[g,k]   = sum over the rows m of group g of dy[m,k]
+ *   dy : [M, K] of `dtype`, rows dy_stride elements apart; x, weight, groups as
+ *        in the forward; mean, rstd : [M] from the forward.
+ *   dx : [M, K] dense of `dtype`; dweight, dbias : [groups, K] dense of
+ *        w_dtype; any of the three may be NULL (not computed).
+ *   workspace : tfq_layer_norm_backward_workspace_bytes(M, K, groups) bytes of
+ *        device memory, 16-byte aligned, needed with dweight or dbias (fp32
+ *        partial sums; contents before and after mean nothing; calls that
+ *        overlap on the GPU need workspaces of their own).
+ * The sums' order depends on the sizes and alignments alone: the same call
+ * gives the same bits.  M == 0 writes zeros to dweight and dbias; K == 0 is a
+ * no-op.  Errors as tfq_layer_norm.
+ */
+TFQ_API size_t tfq_layer_norm_backward_workspace_bytes(int64_t M, int64_t K, int64_t groups);
+TFQ_API tfq_status tfq_layer_norm_backward(const void *dy, int64_t dy_stride, const void *x, int64_t x_stride,
+                                           int dtype, const void *weight, int w_dtype, float weight_offset,
+                                           const float *mean, const float *rstd, int64_t M, int64_t K,
+                                           int64_t groups, void *dx, void *dweight, void *dbias, void *workspace,
+                                           void *stream);
+
+/*
+ * tfq_rope_axes: rotary positions with several axes (time, height, width of a
+ * video's tokens; one axis is the ordinary rotary embedding) on queries and
+ * keys.  Pair i < n_pairs of every head of token m is rotated by
+ *   angle = positions[m, axis[i]] * inv_freq[i]:
+ *   (a, b) -> (a cos - b sin, a sin + b cos)
+ * where (a, b) are elements (2 i, 2 i + 1) (TFQ_ROPE_INTERLEAVED) or
+ * (i, n_pairs + i) (TFQ_ROPE_HALVES) of the head; elements from 2 n_pairs on
+ * are copied.  inverse != 0 rotates back, which is also the gradient: dq =
+ * the inverse rotation of the gradient of q_out.
+ *   q, q_out : [M, q_heads, D] of `dtype` (bf16, fp16, fp32), the D elements of
+ *        a head contiguous, rows and heads at the given strides in elements;
+ *        element-aligned.  q_out may be q itself with the same strides (in
+ *        place); otherwise outputs must not overlap inputs.
+ *   k, k_out : the same with k_heads heads, which need not equal q_heads
+ *        (grouped keys); k_heads == 0: no keys (or, q_heads == 0, no queries).
+ *   positions : [M, n_axes] int32, or int64 with pos_is_64 != 0, at the given
+ *        element strides; any value, negative ones too (|position| < 2^53).
+ *        The angle is formed in 64 bits and reduced there.
+ *   inv_freq, axis : HOST arrays of n_pairs values (read before the call
+ *        returns); axis[i] in [0, n_axes).
+ * M == 0 or no heads is a no-op.
+ * Errors: TFQ_EINVAL (negative sizes, unknown type or pairing, n_pairs < 1 or
+ * 2 n_pairs > D, n_axes < 1, an axis out of range, inv_freq not finite, a null
+ * or not element-aligned pointer), TFQ_EUNSUPPORTED (D > TFQ_ROPE_MAX_D,
+ * q_heads + k_heads > 65536, M >= 2^31, not sm_100).
+ */
+#define TFQ_ROPE_MAX_D 256
+#define TFQ_ROPE_MAX_PAIRS 128
+enum { TFQ_ROPE_INTERLEAVED = 0, TFQ_ROPE_HALVES = 1 };
+TFQ_API tfq_status tfq_rope_axes(const void *q, int64_t q_row_stride, int64_t q_head_stride, int q_heads, void *q_out,
+                                 int64_t q_out_row_stride, int64_t q_out_head_stride, const void *k,
+                                 int64_t k_row_stride, int64_t k_head_stride, int k_heads, void *k_out,
+                                 int64_t k_out_row_stride, int64_t k_out_head_stride, int64_t M, int D, int dtype,
+                                 const void *positions, int pos_is_64, int64_t pos_row_stride,
+                                 int64_t pos_axis_stride, int n_axes, int n_pairs, const double *inv_freq,
+                                 const int32_t *axis, int pairing, int inverse, void *stream);
+
+/*
+ * tfq_scaled_fp8_linear_lora: the scaled FP8 Linear with low-rank adapters of
+ * many requests beside it:
+ *   out[m,n] = bf16_rn(s_a[m] s_w[n] sum_k A_q[m,k] W_q[n,k] + bias[n]
+ *                      + scaling[a] sum_r (sum_k x[m,k] lora_A[a,r,k]) lora_B[a,n,r]),  a = adapter[m].
+ *   A_q, s_a, W_q, s_w, bias_bf16, M, N, K, out_bf16 : as in tfq_scaled_fp8_linear;
+ *       s_a and s_w must be positive (the quantizers' are).
+ *   x_bf16  : [M, K] bf16, the activations the codes A_q were made from.
+ *   lora_A  : [n_adapters, R, K] bf16;  lora_Bs : [n_adapters, N, R] bf16, made
+ *       once per weight by tfq_lora_fold (below): lora_B in units of s_w.
+ *   adapter : [M] int32, one adapter per row, in any order (rows of one request
+ *       one after the other run fastest); a value outside [0, n_adapters)
+ *       means no adapter for that row.
+ *   workspace : tfq_scaled_fp8_linear_lora_workspace_bytes(M, R) bytes of device
+ *       memory, 16-byte aligned (contents before and after mean nothing; calls
+ *       that overlap on the GPU need workspaces of their own).
+ * n_adapters == 0 or R == 0 is tfq_scaled_fp8_linear (x, lora_A, lora_Bs,
+ * adapter and workspace are then not read).  Sums are fp32; the rank-R
+ * intermediate and lora_Bs are bf16 operands of the tensor cores.
+ * M == 0 or N == 0 is a no-op.
+ * Errors: those of tfq_scaled_fp8_linear; TFQ_EINVAL (n_adapters or R negative,
+ * R % 8 != 0, a null pointer, x, lora_A, lora_Bs or workspace not 16-byte
+ * aligned, adapter not 4-byte aligned), TFQ_EUNSUPPORTED (R > TFQ_LORA_MAX_RANK,
+ * n_adapters * max(N, R) >= 2^31).
+ */
+#define TFQ_LORA_MAX_RANK 256
+TFQ_API size_t tfq_scaled_fp8_linear_lora_workspace_bytes(int64_t M, int64_t R);
+TFQ_API tfq_status tfq_scaled_fp8_linear_lora(const void *A_q, const float *s_a, const void *W_q, const float *s_w,
+                                              const void *bias_bf16, int64_t M, int64_t N, int64_t K,
+                                              const void *x_bf16, const void *lora_A, const void *lora_Bs,
+                                              const int32_t *adapter, int64_t n_adapters, int64_t R, void *out_bf16,
+                                              void *workspace, void *stream);
+
+/*
+ * tfq_lora_fold: lora_Bs[a,n,r] = bf16_rn(scaling[a] * lora_B[a,n,r] / s_w[n])
+ * (fp32 product and quotient), once per adapter and weight.
+ *   lora_B, lora_Bs : [n_adapters, N, R] bf16 (lora_Bs may be lora_B: in place);
+ *   scaling : [n_adapters] fp32 or NULL (1);  s_w : [N] fp32.
+ * Errors: TFQ_EINVAL (negative sizes, a null or misaligned pointer: 2 bytes for
+ * bf16, 4 for fp32), TFQ_EUNSUPPORTED (not sm_100).
+ */
+TFQ_API tfq_status tfq_lora_fold(const void *lora_B, const float *scaling, const float *s_w, int64_t n_adapters,
+                                 int64_t N, int64_t R, void *lora_Bs, void *stream);
+
+/*
  * Bytes of the static device array used by tfq_scaled_fp8_linear_noalloc.
  * Every GPU that loads the library holds this array until the process exits.
  */
@@ -388,7 +550,8 @@ TFQ_API const char *tfq_status_string(int status);
 TFQ_API const char *tfq_last_error_message(void);
 
 /* ABI version: 100 * major + minor.  1.1 (101) added tfq_quant_scaled_fp8_linear,
- * tfq_scaled_fp8_linear_multi and tfq_scaled_int8_linear_multi to 1.0. */
+ * tfq_scaled_fp8_linear_multi, tfq_scaled_int8_linear_multi and the operators
+ * around the Linear (layer norm, rotary positions, low-rank adapters) to 1.0. */
 TFQ_API int tfq_version(void);
 
 #ifdef __cplusplus

@@ -23,7 +23,11 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libtfq.so")
 
 TFQ_OK, TFQ_EINVAL, TFQ_EUNSUPPORTED, TFQ_ECUDA, TFQ_ETIMEOUT = range(5)
-TFQ_DTYPE_FP8_E4M3, TFQ_DTYPE_INT8 = 0, 1
+TFQ_DTYPE_FP8_E4M3, TFQ_DTYPE_INT8, TFQ_DTYPE_BF16, TFQ_DTYPE_FP16, TFQ_DTYPE_FP32 = range(5)
+TFQ_ROPE_INTERLEAVED, TFQ_ROPE_HALVES = 0, 1
+TFQ_NORM_MAX_K = 32768
+TFQ_ROPE_MAX_D, TFQ_ROPE_MAX_PAIRS = 256, 128
+TFQ_LORA_MAX_RANK = 256
 TFQ_QUANT_MAX_K = 1 << 24
 TFQ_INT8_MAX_K = 131072  # the INT8 GEMM takes K < this (its s32 sum stays exact)
 TFQ_MULTI_MAX_LINEARS = 4
@@ -44,6 +48,17 @@ SIGNATURES = {
     "tfq_mxfp8_scale_bytes": (_I64, [_I64, _I64]),
     "tfq_quant_mxfp8": (_I, [_P, _I64, _I64, _P, _P, _P]),
     "tfq_mxfp8_linear": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _P]),
+    "tfq_layer_norm": (_I, [_P, _I64, _I, _P, _P, _I, _F, _I64, _I64, _I64, _F, _P, _P, _P, _P]),
+    "tfq_layer_norm_quant_fp8": (_I, [_P, _I64, _I, _P, _P, _I, _F, _I64, _I64, _I64, _F, _F, _P, _P, _P]),
+    "tfq_layer_norm_backward_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
+    "tfq_layer_norm_backward": (_I, [_P, _I64, _P, _I64, _I, _P, _I, _F, _P, _P, _I64, _I64, _I64, _P, _P, _P, _P,
+                                     _P]),
+    "tfq_rope_axes": (_I, [_P, _I64, _I64, _I, _P, _I64, _I64, _P, _I64, _I64, _I, _P, _I64, _I64, _I64, _I, _I, _P,
+                           _I, _I64, _I64, _I, _I, _P, _P, _I, _I, _P]),
+    "tfq_scaled_fp8_linear_lora_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
+    "tfq_scaled_fp8_linear_lora": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _P, _P, _P, _I64, _I64, _P, _P,
+                                        _P]),
+    "tfq_lora_fold": (_I, [_P, _P, _P, _I64, _I64, _I64, _P, _P]),
     "tfq_scaled_fp8_linear_noalloc": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _P]),
     "tfq_selftest_div_rn": (_I, [_P, _P, _I64, _P, _P, _P]),
     "tfq_selftest_wait_timeout": (_I, [ctypes.c_uint32, _P]),

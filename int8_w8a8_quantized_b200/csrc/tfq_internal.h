@@ -151,4 +151,57 @@ tfq_status launch_scaled_int8_gemm(const void* A, const float* s_a, const void* 
                                    const void* bias, int64_t M, int64_t N, int64_t K, void* out,
                                    cudaStream_t stream, DeviceState* ds);
 
+// Layer norm (tfq_norm.cu): the operands its forms share.  Strides are in
+// elements; w and b are [groups, K] of w_dtype (dtype or fp32), M % groups == 0.
+struct NormCall {
+    const void* x;
+    int64_t x_stride;
+    int dtype;
+    const void* w;
+    const void* b;
+    int w_dtype;
+    float offset;
+    int64_t M, K, groups;
+    float eps;
+    float* mean;
+    float* rstd;
+};
+
+// y (of x's type), or with q non-null E4M3 codes q and scales s (y unused).
+tfq_status launch_layer_norm(const NormCall& c, void* y, uint8_t* q, float* s, float qmax, cudaStream_t stream,
+                             DeviceState* ds);
+
+// dx, dw, db, any of them null; workspace of layer_norm_backward_workspace() bytes (with dw or db).
+int64_t layer_norm_backward_workspace(int64_t M, int64_t K, int64_t groups);
+tfq_status launch_layer_norm_backward(const NormCall& c, const void* dy, int64_t dy_stride, void* dx, void* dw,
+                                      void* db, float* workspace, cudaStream_t stream, DeviceState* ds);
+
+// Rotary positions (tfq_rope.cu).  [M, heads, D] with element strides; heads == 0: absent.
+struct RopeTensor {
+    const void* in;
+    void* out;
+    int64_t row_stride, head_stride, out_row_stride, out_head_stride;
+    int heads;
+};
+tfq_status launch_rope(const RopeTensor& q, const RopeTensor& k, int64_t M, int D, int dtype, const void* pos,
+                       bool pos64, int64_t pos_row_stride, int64_t pos_axis_stride, int pairs, const double* inv_freq,
+                       const int32_t* axis, bool halves, bool inverse, cudaStream_t stream);
+
+// Low-rank adapters (tfq_lora.cu): Bs = bf16(scaling[a] B / s_w[n]), and the
+// scaled FP8 Linear with one adapter per row beside it.
+struct LoraCall {
+    const void* x;        // [M, K] bf16
+    const void* A;        // [n_adapters, R, K] bf16
+    const void* Bs;       // [n_adapters, N, R] bf16
+    const int32_t* idx;   // [M]; outside [0, n_adapters): no adapter
+    int n_adapters, R;
+    void* workspace;
+};
+tfq_status launch_lora_fold(const void* B, const float* scaling, const float* s_w, int64_t n, int64_t N, int64_t R,
+                            void* Bs, cudaStream_t stream);
+size_t lora_workspace_bytes(int64_t M, int64_t R);
+tfq_status launch_scaled_fp8_lora(const void* A_q, const float* s_a, const void* W_q, const float* s_w,
+                                  const void* bias, int64_t M, int64_t N, int64_t K, const LoraCall& l, void* out,
+                                  cudaStream_t stream, DeviceState* ds);
+
 }  // namespace tfq

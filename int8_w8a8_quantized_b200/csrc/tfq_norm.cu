@@ -1,0 +1,706 @@
+// tfq_norm.cu -- layer norm around the W8A8 Linear: forward, straight to
+// per-token E4M3 codes, and backward with the weight and bias gradients.
+//
+// For a row x[0..K) of group g (M rows in G groups of equally many rows; G = 1
+// is the ordinary norm, G > 1 the adaptive norm whose weight and bias come
+// from a condition of each sample):
+//   mean = 1/K sum x,  rstd = 1 / sqrt(1/K sum (x - mean)^2 + eps)
+//   xhat = (x - mean) rstd,  y = xhat (w[g] + offset) + b[g]
+// and, with h = dy (w[g] + offset),
+//   dx    = rstd (h - 1/K sum h - xhat 1/K sum h xhat)
+//   dw[g] = sum over the group's rows of dy xhat,  db[g] = ... of dy.
+// The quantizing form writes s = fl32(max(max |y|, 1e-12) / qmax) and the
+// E4M3 code of y / s, y being the fp32 value above (not rounded to the input's
+// type in between: one rounding fewer than norm and quantizer as two calls,
+// and the M x K intermediate is neither written nor read).
+//
+// All sums, the statistics and the gradients' partial sums are fp32.  The
+// variance is summed from x - mean (two passes over a row that stays in
+// registers), so a large common offset costs no digits.
+//
+// Bound by HBM: a row is read once into registers.  A row belongs to `tpr`
+// threads: a power of two up to 32 (several rows per warp, no barrier) or a
+// whole CTA of up to 1024; thread t holds the row's 16-byte units t, t + tpr,
+// ... (J at most).  CTAs walk consecutive rows and load the next row before
+// they reduce the present one.  The weight and bias are read again for every
+// row: they stay in L1 (the row loads do not allocate there).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "tfq_internal.h"
+#include "tfq_ptx.cuh"
+#include "tfq_quant_common.cuh"
+#include "tfq_quant_row.cuh"
+
+namespace tfq {
+namespace {
+
+// ------------------------------------------------- units of a row
+// VEC elements of type T: one 16-byte unit (VEC * sizeof(T) == 16) or, for
+// rows that are not 16-byte aligned, one element.
+template <typename T>
+__device__ __forceinline__ float to_float(T v) {
+    if constexpr (sizeof(T) == 4) return v;
+    else if constexpr (std::is_same_v<T, __half>) return __half2float(v);
+    else return __bfloat162float(v);
+}
+template <typename T>
+__device__ __forceinline__ T from_float(float v) {
+    if constexpr (sizeof(T) == 4) return v;
+    else if constexpr (std::is_same_v<T, __half>) return __float2half_rn(v);
+    else return __float2bfloat16_rn(v);
+}
+
+// One element through the read-only path.  (The 16-bit types' own __ldg is an
+// asm statement without side effects, which the compiler may move in front of
+// the test that guards it: a load through a null pointer or past the row.)
+template <typename T>
+__device__ __forceinline__ T ldg_elem(const T* p) {
+    if constexpr (sizeof(T) == 4) {
+        return __ldg(p);
+    } else {
+        const unsigned short w = __ldg(reinterpret_cast<const unsigned short*>(p));
+        return *reinterpret_cast<const T*>(&w);
+    }
+}
+
+template <typename T, int VEC>
+struct Unit {
+    static_assert(VEC == 1 || VEC * sizeof(T) == 16, "a unit is one element or 16 bytes");
+    using Raw = std::conditional_t<VEC == 1, T, uint4>;
+    Raw raw;
+
+    __device__ __forceinline__ void clear() {
+        if constexpr (VEC == 1) raw = from_float<T>(0.0f);
+        else raw = make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ __forceinline__ void load(const T* row, int u) {
+        if constexpr (VEC == 1) raw = ldg_elem(row + u);
+        else raw = ldg_nc_v4(reinterpret_cast<const uint4*>(row) + u);
+    }
+    __device__ __forceinline__ void get(float (&f)[VEC]) const {
+        if constexpr (VEC == 1) {
+            f[0] = to_float<T>(raw);
+        } else {
+            const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (sizeof(T) == 4) {
+                    f[i] = __uint_as_float(w[i]);
+                } else if constexpr (std::is_same_v<T, __half>) {
+                    const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                    f[2 * i] = p.x;
+                    f[2 * i + 1] = p.y;
+                } else {
+                    f[2 * i] = bf16_lo(w[i]);
+                    f[2 * i + 1] = bf16_hi(w[i]);
+                }
+            }
+        }
+    }
+    static __device__ __forceinline__ void store(T* row, int u, const float (&f)[VEC]) {
+        if constexpr (VEC == 1) {
+            row[u] = from_float<T>(f[0]);
+        } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (sizeof(T) == 4) {
+                    w[i] = __float_as_uint(f[i]);
+                } else if constexpr (std::is_same_v<T, __half>) {
+                    const __half2 p = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+                    w[i] = *reinterpret_cast<const uint32_t*>(&p);
+                } else {
+                    const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+                    w[i] = *reinterpret_cast<const uint32_t*>(&p);
+                }
+            }
+            reinterpret_cast<uint4*>(row)[u] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+};
+
+// VEC values of a weight or bias row (of the input's type, or fp32) from
+// column c; in the vector form their addresses are 16-byte aligned.
+template <typename T, int VEC>
+__device__ __forceinline__ void load_affine(float (&f)[VEC], const void* base, bool f32, int64_t at) {
+    if (f32) {
+        const float* p = static_cast<const float*>(base) + at;
+        if constexpr (VEC == 1) {
+            f[0] = __ldg(p);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC / 4; ++i) {
+                const float4 v = __ldg(reinterpret_cast<const float4*>(p) + i);
+                f[4 * i] = v.x;
+                f[4 * i + 1] = v.y;
+                f[4 * i + 2] = v.z;
+                f[4 * i + 3] = v.w;
+            }
+        }
+    } else {
+        const T* p = static_cast<const T*>(base) + at;
+        Unit<T, VEC> u;
+        if constexpr (VEC == 1) u.raw = ldg_elem(p);
+        else u.raw = __ldg(reinterpret_cast<const uint4*>(p));
+        u.get(f);
+    }
+}
+
+// ------------------------------------------------- sums over a row's threads
+// kWarpRow: the row's tpr (a power of two, <= 32) lanes; otherwise the whole
+// CTA, through `red` (32 floats per reduction, zero past the CTA's warps).
+// Every thread gets the result, summed in an order that depends only on the
+// launch shape.  Consecutive calls need different `red` buffers: a buffer may
+// be written again only after another reduction's barrier.
+struct SumOp {
+    static __device__ __forceinline__ float apply(float a, float b) { return a + b; }
+};
+struct MaxOp {
+    static __device__ __forceinline__ float apply(float a, float b) { return fmaxf(a, b); }
+};
+
+template <bool kWarpRow, typename Op, int N>
+__device__ __forceinline__ void row_reduce(float (&v)[N], int tpr, float* red) {
+    if constexpr (kWarpRow) {
+        for (int o = tpr >> 1; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = Op::apply(v[i], __shfl_xor_sync(0xFFFFFFFFu, v[i], o));
+    } else {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = Op::apply(v[i], __shfl_xor_sync(0xFFFFFFFFu, v[i], o));
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int i = 0; i < N; ++i) red[32 * i + (threadIdx.x >> 5)] = v[i];
+        __syncthreads();
+        const int quads = (static_cast<int>(blockDim.x >> 5) + 3) >> 2;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float s = 0.0f;
+            for (int q = 0; q < quads; ++q) {
+                const float4 p = *reinterpret_cast<const float4*>(red + 32 * i + 4 * q);
+                s = Op::apply(s, Op::apply(Op::apply(p.x, p.y), Op::apply(p.z, p.w)));
+            }
+            v[i] = s;
+        }
+    }
+}
+
+struct NormArgs {
+    const void* x;
+    int64_t x_stride;  // elements between rows
+    const void* w;     // [G, K] or null
+    const void* b;     // [G, K] or null
+    int w_f32;         // w and b (and their gradients) are fp32, else of the input's type
+    float offset;
+    int64_t M;
+    int64_t group_rows;
+    int K;
+    int tpr;    // threads per row
+    float eps;
+    float* mean;  // [M] or null (written by the forward, read by the backward)
+    float* rstd;
+    // forward
+    void* y;  // [M, K]
+    // quantizing forward
+    uint8_t* q;  // [M, K]
+    float* s;    // [M]
+    float qmax;
+    int clamp;  // qmax is not an E4M3 value
+    // backward
+    const void* dy;
+    int64_t dy_stride;
+    void* dx;        // [M, K] or null
+    float* part_dw;  // [G, parts, K] partial sums, or null
+    float* part_db;
+    int parts;
+};
+
+// Rows per CTA at a time, and this thread's place: row slot and lane in it.
+template <bool kWarpRow>
+__device__ __forceinline__ void my_place(int tpr, int& slots, int& slot, int& t) {
+    if constexpr (kWarpRow) {
+        slots = blockDim.x / tpr;
+        slot = threadIdx.x / tpr;
+        t = threadIdx.x & (tpr - 1);
+    } else {
+        slots = 1;
+        slot = 0;
+        t = threadIdx.x;
+    }
+}
+
+template <typename T, int VEC, int J, bool kWarpRow, bool kQuant>
+__global__ void __launch_bounds__(J > 4 ? 1024 : 512)
+    norm_forward_kernel(const NormArgs p) {
+    __shared__ __align__(16) float red[3][32];
+    int slots, slot, t;
+    my_place<kWarpRow>(p.tpr, slots, slot, t);
+    if constexpr (!kWarpRow)
+        for (int i = threadIdx.x; i < 96; i += blockDim.x) (&red[0][0])[i] = 0.0f;
+    pdl_allow_next();
+    pdl_wait();
+    const int units = p.K / VEC;
+    // consecutive rows per CTA, so that a group's weight and bias stay in L1
+    const int64_t chunk = (p.M + static_cast<int64_t>(gridDim.x) * slots - 1) / (static_cast<int64_t>(gridDim.x) * slots) * slots;
+    const int64_t first = blockIdx.x * chunk;
+    const int64_t last = min(p.M, first + chunk);
+    const float inv_k = 1.0f / static_cast<float>(p.K);
+    Unit<T, VEC> cur[J];
+    const auto fetch = [&](Unit<T, VEC>(&v)[J], int64_t r) {
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int u = t + p.tpr * j;
+            v[j].clear();
+            if (r < last && u < units) v[j].load(static_cast<const T*>(p.x) + r * p.x_stride, u);
+        }
+    };
+    if constexpr (!kWarpRow) __syncthreads();  // red cleared
+    fetch(cur, first + slot);
+    for (int64_t base = first; base < last; base += slots) {
+        const int64_t r = base + slot;
+        Unit<T, VEC> next[J];
+        fetch(next, r + slots);
+        float acc[1] = {0.0f};
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            float f[VEC];
+            cur[j].get(f);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) acc[0] += f[i];
+        }
+        row_reduce<kWarpRow, SumOp>(acc, p.tpr, red[0]);
+        const float mean = acc[0] * inv_k;
+        acc[0] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            if (t + p.tpr * j < units) {
+                float f[VEC];
+                cur[j].get(f);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const float d = f[i] - mean;
+                    acc[0] = fmaf(d, d, acc[0]);
+                }
+            }
+        }
+        row_reduce<kWarpRow, SumOp>(acc, p.tpr, red[1]);
+        const float rstd = __frsqrt_rn(fmaf(acc[0], inv_k, p.eps));
+        const bool row_ok = r < last;
+        if (p.mean != nullptr && row_ok && t == 0) {
+            p.mean[r] = mean;
+            p.rstd[r] = rstd;
+        }
+        int64_t affine = 0;  // M < 2^31: a 32-bit division
+        if (p.group_rows != p.M && row_ok)
+            affine = static_cast<int64_t>(static_cast<uint32_t>(r) / static_cast<uint32_t>(p.group_rows)) * p.K;
+        const auto value = [&](int j, float(&y)[VEC]) {
+            const int64_t at = affine + static_cast<int64_t>(t + p.tpr * j) * VEC;
+            cur[j].get(y);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) y[i] = (y[i] - mean) * rstd;
+            if (p.w != nullptr) {
+                float w[VEC];
+                load_affine<T, VEC>(w, p.w, p.w_f32, at);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) y[i] *= w[i] + p.offset;
+            }
+            if (p.b != nullptr) {
+                float b[VEC];
+                load_affine<T, VEC>(b, p.b, p.w_f32, at);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) y[i] += b[i];
+            }
+        };
+        if constexpr (!kQuant) {
+            if (row_ok) {
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    if (t + p.tpr * j < units) {
+                        float y[VEC];
+                        value(j, y);
+                        Unit<T, VEC>::store(static_cast<T*>(p.y) + r * p.K, t + p.tpr * j, y);
+                    }
+                }
+            }
+        } else {
+            // up to four units a thread the values wait in registers for the
+            // row's maximum; more are computed a second time
+            constexpr bool kKeep = J * VEC <= 32;
+            float y[kKeep ? J : 1][VEC];
+            float amax[1] = {0.0f};
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                if (t + p.tpr * j < units) {
+                    value(j, y[kKeep ? j : 0]);
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) amax[0] = fmaxf(amax[0], fabsf(y[kKeep ? j : 0][i]));
+                }
+            }
+            row_reduce<kWarpRow, MaxOp>(amax, p.tpr, red[2]);
+            const float sc = __fdiv_rn(fmaxf(amax[0], 1e-12f), p.qmax);
+            if (row_ok) {
+                if (t == 0) p.s[r] = sc;
+                const float rcp = __frcp_rn(sc);
+                const float rcp_lo = rcp_low(sc, rcp);
+                const bool ieee = !(sc <= kDivMaxScale);
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    const int u = t + p.tpr * j;
+                    if (u >= units) continue;
+                    if constexpr (!kKeep) value(j, y[0]);
+                    const float(&yj)[VEC] = y[kKeep ? j : 0];
+                    uint32_t codes[(VEC + 1) / 2];
+#pragma unroll
+                    for (int i = 0; i < VEC; i += 2) {
+                        const float a = yj[i], b = VEC > 1 ? yj[(i + 1) % VEC] : 0.0f;
+                        float2 d = ieee ? make_float2(__fdiv_rn(a, sc), __fdiv_rn(b, sc))
+                                        : div2_rn_unsigned_zero(make_float2(a, b), sc, rcp, rcp_lo);
+                        if (p.clamp) {
+                            d.x = fminf(fmaxf(d.x, -p.qmax), p.qmax);
+                            d.y = fminf(fmaxf(d.y, -p.qmax), p.qmax);
+                        }
+                        codes[i / 2] = cvt_e4m3x2(d.x, d.y);
+                    }
+                    uint8_t* out = p.q + r * p.K;
+                    if constexpr (VEC == 8) {
+                        reinterpret_cast<uint2*>(out)[u] =
+                            make_uint2(codes[0] | (codes[1] << 16), codes[2] | (codes[3] << 16));
+                    } else if constexpr (VEC == 4) {
+                        reinterpret_cast<uint32_t*>(out)[u] = codes[0] | (codes[1] << 16);
+                    } else {
+                        out[u] = static_cast<uint8_t>(codes[0]);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < J; ++j) cur[j] = next[j];
+    }
+}
+
+// Backward.  Grid G * parts: CTA (g, i) walks the i-th share of group g's
+// rows; a thread owns the same columns of every row, so the sums for dw and db
+// stay in its registers and leave once per CTA, as fp32 partials [g][i][K]
+// that norm_partials_kernel adds up in order of i.
+template <typename T, int VEC, int J, bool kWarpRow>
+__global__ void __launch_bounds__(J > 4 ? 1024 : 512)
+    norm_backward_kernel(const NormArgs p) {
+    __shared__ __align__(16) float red[2][64];
+    int slots, slot, t;
+    my_place<kWarpRow>(p.tpr, slots, slot, t);
+    if constexpr (!kWarpRow)
+        for (int i = threadIdx.x; i < 128; i += blockDim.x) (&red[0][0])[i] = 0.0f;
+    pdl_allow_next();
+    pdl_wait();
+    const int units = p.K / VEC;
+    const int64_t g = blockIdx.x / static_cast<unsigned>(p.parts);
+    const int64_t part = blockIdx.x % static_cast<unsigned>(p.parts);
+    const int64_t chunk = (p.group_rows + p.parts - 1) / p.parts;
+    const int64_t first = g * p.group_rows + part * chunk;
+    const int64_t last = min((g + 1) * p.group_rows, first + chunk);
+    const float inv_k = 1.0f / static_cast<float>(p.K);
+    float dw[J][VEC], db[J][VEC];
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) dw[j][i] = db[j][i] = 0.0f;
+    if constexpr (!kWarpRow) __syncthreads();  // red cleared
+    int turn = 0;
+    for (int64_t base = first; base < last; base += slots, turn ^= 1) {
+        const int64_t r = base + slot;
+        const bool row_ok = r < last;
+        Unit<T, VEC> ux[J], ud[J];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int u = t + p.tpr * j;
+            ux[j].clear();
+            ud[j].clear();
+            if (row_ok && u < units) {
+                ux[j].load(static_cast<const T*>(p.x) + r * p.x_stride, u);
+                ud[j].load(static_cast<const T*>(p.dy) + r * p.dy_stride, u);
+            }
+        }
+        const float mean = row_ok ? __ldg(p.mean + r) : 0.0f;
+        const float rstd = row_ok ? __ldg(p.rstd + r) : 0.0f;
+        float acc[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            if (row_ok && t + p.tpr * j < units) {
+                float x[VEC], d[VEC], w[VEC];
+                ux[j].get(x);
+                ud[j].get(d);
+                if (p.w != nullptr) load_affine<T, VEC>(w, p.w, p.w_f32, g * p.K + (t + p.tpr * j) * VEC);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const float xhat = (x[i] - mean) * rstd;
+                    dw[j][i] = fmaf(d[i], xhat, dw[j][i]);
+                    db[j][i] += d[i];
+                    const float h = p.w != nullptr ? d[i] * (w[i] + p.offset) : d[i];
+                    acc[0] += h;
+                    acc[1] = fmaf(h, xhat, acc[1]);
+                }
+            }
+        }
+        if (p.dx != nullptr) {
+            row_reduce<kWarpRow, SumOp>(acc, p.tpr, red[turn]);
+            const float c1 = acc[0] * inv_k, c2 = acc[1] * inv_k;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                if (row_ok && t + p.tpr * j < units) {
+                    float x[VEC], d[VEC], w[VEC];
+                    ux[j].get(x);
+                    ud[j].get(d);
+                    if (p.w != nullptr) load_affine<T, VEC>(w, p.w, p.w_f32, g * p.K + (t + p.tpr * j) * VEC);
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) {
+                        const float xhat = (x[i] - mean) * rstd;
+                        const float h = p.w != nullptr ? d[i] * (w[i] + p.offset) : d[i];
+                        d[i] = rstd * (h - c1 - xhat * c2);
+                    }
+                    Unit<T, VEC>::store(static_cast<T*>(p.dx) + r * p.K, t + p.tpr * j, d);
+                }
+            }
+        }
+    }
+    if (p.part_dw == nullptr && p.part_db == nullptr) return;
+    const int64_t out = (g * p.parts + part) * p.K;
+    if constexpr (!kWarpRow) {
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int u = t + p.tpr * j;
+            if (u < units) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    if (p.part_dw != nullptr) p.part_dw[out + u * VEC + i] = dw[j][i];
+                    if (p.part_db != nullptr) p.part_db[out + u * VEC + i] = db[j][i];
+                }
+            }
+        }
+    } else {
+        // the rows of one warp by shuffles, then the warps in order
+        __shared__ float cols[2][32 * J * VEC];
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                for (int o = p.tpr; o < 32; o <<= 1) {
+                    dw[j][i] += __shfl_xor_sync(0xFFFFFFFFu, dw[j][i], o);
+                    db[j][i] += __shfl_xor_sync(0xFFFFFFFFu, db[j][i], o);
+                }
+        const int lane = threadIdx.x & 31;
+        for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) {
+            if (static_cast<int>(threadIdx.x >> 5) == w && lane < p.tpr) {
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) {
+                        const int c = (t + p.tpr * j) * VEC + i;
+                        cols[0][c] = (w == 0 ? 0.0f : cols[0][c]) + dw[j][i];
+                        cols[1][c] = (w == 0 ? 0.0f : cols[1][c]) + db[j][i];
+                    }
+            }
+            __syncthreads();
+        }
+        for (int c = threadIdx.x; c < p.K; c += blockDim.x) {
+            if (p.part_dw != nullptr) p.part_dw[out + c] = cols[0][c];
+            if (p.part_db != nullptr) p.part_db[out + c] = cols[1][c];
+        }
+    }
+}
+
+// dw[g, c] = sum over i of part_dw[g][i][c], and db likewise: 32 columns per
+// CTA, the parts split over 8 warps and joined in order.
+template <typename T>
+__global__ void __launch_bounds__(256) norm_partials_kernel(const float* part_dw, const float* part_db, int K,
+                                                            int parts, int w_f32, void* dw, void* db) {
+    __shared__ float sums[8][33];
+    pdl_allow_next();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const unsigned blocks = static_cast<unsigned>(K + 31) / 32;
+    const int c = static_cast<int>(blockIdx.x % blocks) * 32 + lane;
+    const int64_t g = blockIdx.x / blocks;
+    const float* part = blockIdx.y == 0 ? part_dw : part_db;
+    void* dst = blockIdx.y == 0 ? dw : db;
+    if (part == nullptr) return;
+    float s = 0.0f;
+    if (c < K)
+        for (int i = warp; i < parts; i += 8) s += part[(g * parts + i) * K + c];
+    sums[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && c < K) {
+        s = sums[0][lane];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) s += sums[i][lane];
+        if (w_f32) static_cast<float*>(dst)[g * K + c] = s;
+        else static_cast<T*>(dst)[g * K + c] = from_float<T>(s);
+    }
+}
+
+// ------------------------------------------------- launch shapes
+struct NormShape {
+    bool vec;   // 16-byte units
+    int j;      // units per thread
+    int tpr;    // threads per row
+    int block;  // threads per CTA
+};
+
+// Threads per row: a power of two up to 32 where J = 2 units each cover the
+// row, else whole warps; J = 2, or more where a row needs over 512 threads.
+NormShape norm_shape(int64_t K, int elem, bool vec) {
+    const int units = static_cast<int>(vec ? K * elem / 16 : K);
+    if (units <= 64) {
+        int tpr = 1;
+        while (2 * tpr < units) tpr *= 2;
+        return {vec, 2, tpr, 256};
+    }
+    for (int j : {2, 4, 8}) {
+        if (j == 4 && !vec) continue;
+        const int tpr = ((units + j - 1) / j + 31) / 32 * 32;
+        if (tpr <= (j <= 4 ? 512 : 1024)) return {vec, j, tpr, tpr};
+    }
+    return {vec, 32, 1024, 1024};  // scalar units, K <= TFQ_NORM_MAX_K
+}
+
+tfq_status launch_error(const char* what, cudaError_t e) {
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return e == cudaSuccess ? TFQ_OK : fail(TFQ_ECUDA, "%s launch: %s", what, cudaGetErrorString(e));
+}
+
+using NormKernel = void (*)(const NormArgs);
+
+template <typename T, bool kQuant>
+NormKernel forward_kernel(const NormShape& s) {
+    constexpr int V = 16 / sizeof(T);
+    if (s.vec) {
+        if (s.block == 256 && s.tpr <= 32) return norm_forward_kernel<T, V, 2, true, kQuant>;
+        return s.j == 2   ? norm_forward_kernel<T, V, 2, false, kQuant>
+               : s.j == 4 ? norm_forward_kernel<T, V, 4, false, kQuant>
+                          : norm_forward_kernel<T, V, 8, false, kQuant>;
+    }
+    if (s.block == 256 && s.tpr <= 32) return norm_forward_kernel<T, 1, 2, true, kQuant>;
+    if (s.j == 2) return norm_forward_kernel<T, 1, 2, false, kQuant>;
+    return s.j == 8 ? norm_forward_kernel<T, 1, 8, false, kQuant> : norm_forward_kernel<T, 1, 32, false, kQuant>;
+}
+
+template <typename T>
+NormKernel backward_kernel(const NormShape& s) {
+    constexpr int V = 16 / sizeof(T);
+    if (s.vec) {
+        if (s.block == 256 && s.tpr <= 32) return norm_backward_kernel<T, V, 2, true>;
+        return s.j == 2   ? norm_backward_kernel<T, V, 2, false>
+               : s.j == 4 ? norm_backward_kernel<T, V, 4, false>
+                          : norm_backward_kernel<T, V, 8, false>;
+    }
+    if (s.block == 256 && s.tpr <= 32) return norm_backward_kernel<T, 1, 2, true>;
+    if (s.j == 2) return norm_backward_kernel<T, 1, 2, false>;
+    return s.j == 8 ? norm_backward_kernel<T, 1, 8, false> : norm_backward_kernel<T, 1, 32, false>;
+}
+
+int elem_size(int dtype) { return dtype == TFQ_DTYPE_FP32 ? 4 : 2; }
+
+// The vector form needs every row of every operand on a 16-byte boundary.
+bool rows_aligned(const void* p, int64_t stride, int elem) { return p == nullptr || (aligned16(p) && stride * elem % 16 == 0); }
+
+bool norm_vector_ok(const NormCall& c, const void* out, int64_t out_elem) {
+    const int e = elem_size(c.dtype);
+    const int we = elem_size(c.w_dtype);
+    return c.K * e % 16 == 0 && rows_aligned(c.x, c.x_stride, e) && rows_aligned(c.w, c.K, we) &&
+           rows_aligned(c.b, c.K, we) && (out == nullptr || aligned16(out)) && out_elem * c.K % 4 == 0;
+}
+
+NormArgs norm_args(const NormCall& c, const NormShape& s) {
+    NormArgs a = {};
+    a.x = c.x;
+    a.x_stride = c.x_stride;
+    a.w = c.w;
+    a.b = c.b;
+    a.w_f32 = c.w_dtype == TFQ_DTYPE_FP32;
+    a.offset = c.offset;
+    a.M = c.M;
+    a.group_rows = c.M / c.groups;
+    a.K = static_cast<int>(c.K);
+    a.tpr = s.tpr;
+    a.eps = c.eps;
+    a.mean = c.mean;
+    a.rstd = c.rstd;
+    return a;
+}
+
+// CTAs per SM worth launching: about 1536 threads.
+int64_t norm_grid(const NormShape& s, int64_t rows, int sm_count) {
+    const int64_t slots = s.block / s.tpr;
+    return std::min<int64_t>((rows + slots - 1) / slots, static_cast<int64_t>(sm_count) * std::max(1, 1536 / s.block));
+}
+
+}  // namespace
+
+tfq_status launch_layer_norm(const NormCall& c, void* y, uint8_t* q, float* s, float qmax, cudaStream_t stream,
+                             DeviceState* ds) {
+    const int e = elem_size(c.dtype);
+    const NormShape sh = norm_shape(c.K, e, norm_vector_ok(c, q != nullptr ? q : y, q != nullptr ? 1 : e));
+    NormArgs a = norm_args(c, sh);
+    a.y = y;
+    a.q = q;
+    a.s = s;
+    a.qmax = qmax;
+    a.clamp = q != nullptr && !is_e4m3_value(qmax);
+    NormKernel k;
+    if (c.dtype == TFQ_DTYPE_FP32) k = q ? forward_kernel<float, true>(sh) : forward_kernel<float, false>(sh);
+    else if (c.dtype == TFQ_DTYPE_FP16) k = q ? forward_kernel<__half, true>(sh) : forward_kernel<__half, false>(sh);
+    else k = q ? forward_kernel<__nv_bfloat16, true>(sh) : forward_kernel<__nv_bfloat16, false>(sh);
+    return launch_error("layer norm", launch_kernel(k, dim3(static_cast<unsigned>(norm_grid(sh, c.M, ds->sm_count))),
+                                                    dim3(sh.block), 0, stream, a));
+}
+
+// Row shares per group of the backward: enough CTAs to fill the GPU once, each
+// with rows for every slot of the CTA.
+constexpr int kNormMaxSms = 160;  // the workspace formula knows no device: more SMs add no parts
+static int64_t backward_parts(int64_t M, int64_t groups, const NormShape& s, int sm_count) {
+    const int64_t slots = s.block / s.tpr;
+    const int64_t ctas = static_cast<int64_t>(std::min(sm_count, kNormMaxSms)) * std::max(1, std::min(8, 1024 / s.block));
+    return std::max<int64_t>(1, std::min<int64_t>((M / groups + slots - 1) / slots, (ctas + groups - 1) / groups));
+}
+
+int64_t layer_norm_backward_workspace(int64_t M, int64_t K, int64_t groups) {
+    int64_t parts = 1;  // the most that any type and alignment of the operands takes
+    for (int e : {2, 4})
+        for (bool vec : {true, false})
+            parts = std::max(parts, backward_parts(M, groups, norm_shape(K, e, vec), kNormMaxSms));
+    return 2 * groups * parts * K * 4;
+}
+
+tfq_status launch_layer_norm_backward(const NormCall& c, const void* dy, int64_t dy_stride, void* dx, void* dw,
+                                      void* db, float* workspace, cudaStream_t stream, DeviceState* ds) {
+    const int e = elem_size(c.dtype);
+    const bool vec = norm_vector_ok(c, dx, e) && rows_aligned(dy, dy_stride, e);
+    const NormShape sh = norm_shape(c.K, e, vec);
+    NormArgs a = norm_args(c, sh);
+    a.dy = dy;
+    a.dy_stride = dy_stride;
+    a.dx = dx;
+    a.parts = static_cast<int>(backward_parts(c.M, c.groups, sh, ds->sm_count));
+    const int64_t n = c.groups * a.parts * c.K;
+    a.part_dw = dw != nullptr ? workspace : nullptr;
+    a.part_db = db != nullptr ? workspace + (dw != nullptr ? n : 0) : nullptr;
+    NormKernel k = c.dtype == TFQ_DTYPE_FP32 ? backward_kernel<float>(sh)
+                   : c.dtype == TFQ_DTYPE_FP16 ? backward_kernel<__half>(sh) : backward_kernel<__nv_bfloat16>(sh);
+    const dim3 grid(static_cast<unsigned>(a.parts * c.groups));
+    tfq_status st = launch_error("layer norm backward", launch_kernel(k, grid, dim3(sh.block), 0, stream, a));
+    if (st != TFQ_OK || (dw == nullptr && db == nullptr)) return st;
+    auto join = c.dtype == TFQ_DTYPE_FP32 ? norm_partials_kernel<float>
+                : c.dtype == TFQ_DTYPE_FP16 ? norm_partials_kernel<__half> : norm_partials_kernel<__nv_bfloat16>;
+    const dim3 jgrid(static_cast<unsigned>((c.K + 31) / 32 * c.groups), 2);
+    return launch_error("layer norm gradient", launch_kernel(join, jgrid, dim3(256), 0, stream,
+                                                             const_cast<const float*>(a.part_dw),
+                                                             const_cast<const float*>(a.part_db), a.K, a.parts,
+                                                             a.w_f32, dw, db));
+}
+
+}  // namespace tfq

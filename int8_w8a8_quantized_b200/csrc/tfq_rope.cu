@@ -1,0 +1,253 @@
+// tfq_rope.cu -- rotary positions with several axes (time, height, width, ...)
+// on the queries and keys of an attention layer, in one launch.
+//
+// Rotated pair i of a head (i < P) belongs to one axis of the token's
+// position: angle = position[axis[i]] * inv_freq[i], and
+//   (a, b) -> (a cos - b sin, a sin + b cos)
+// with (a, b) = elements (2 i, 2 i + 1) or (i, P + i) of the head; elements
+// from 2 P on are copied.  The inverse rotation (sin negated) is the
+// operator's gradient: a rotation's transpose is its inverse.
+//
+// Positions reach millions of turns, where an fp32 angle has lost its
+// fraction: the angle is formed in fp64 as position * (inv_freq / 2 pi), its
+// whole turns are dropped there, and only the fraction goes to fp32 for
+// sincospi.  That costs one fp64 product per token and pair, not per element.
+//
+// Bound by HBM: every element is read and written once.  A CTA takes a few
+// tokens; its threads form the tokens' cos/sin table in shared memory (one
+// or a few entries each), then stream the heads: a thread stays at one place
+// within the head, so it reads its table entries once per token and uses
+// them for every head.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "tfq_internal.h"
+#include "tfq_ptx.cuh"
+#include "tfq_quant_common.cuh"
+
+namespace tfq {
+namespace {
+
+constexpr int kRopeThreads = 256;
+
+struct RopeArgs {
+    RopeTensor q, k;
+    int64_t M;
+    int D;
+    int pairs;
+    int items;       // places within a head: units of the rotated part, then of the copied part
+    int rot_items;   // the first of them that rotate
+    int head_lanes;  // heads of one token processed at a time
+    int tokens;      // tokens per CTA
+    int inverse;
+    const void* pos;
+    int pos64;
+    int64_t pos_row_stride, pos_axis_stride;
+    double inv_turn[TFQ_ROPE_MAX_PAIRS];  // inv_freq / (2 pi)
+    uint8_t axis[TFQ_ROPE_MAX_PAIRS];
+};
+
+template <typename T, int VEC>
+struct Chunk {  // VEC elements of T, moved as one 16-byte access (VEC > 1) or one element
+    using Raw = std::conditional_t<VEC == 1, T, uint4>;
+    Raw raw;
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (VEC == 1) {
+            raw = *p;
+        } else {  // not the read-only path: the call may be in place
+            asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(raw.x), "=r"(raw.y), "=r"(raw.z), "=r"(raw.w)
+                         : "l"(p));
+        }
+    }
+    __device__ __forceinline__ void store(T* p) const {
+        if constexpr (VEC == 1) *p = raw;
+        else *reinterpret_cast<uint4*>(p) = raw;
+    }
+    __device__ __forceinline__ void get(float (&f)[VEC]) const {
+        const T* e = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            if constexpr (sizeof(T) == 4) f[i] = e[i];
+            else if constexpr (std::is_same_v<T, __half>) f[i] = __half2float(e[i]);
+            else f[i] = __bfloat162float(e[i]);
+        }
+    }
+    __device__ __forceinline__ void set(const float (&f)[VEC]) {
+        T* e = reinterpret_cast<T*>(&raw);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            if constexpr (sizeof(T) == 4) e[i] = f[i];
+            else if constexpr (std::is_same_v<T, __half>) e[i] = __float2half_rn(f[i]);
+            else e[i] = __float2bfloat16_rn(f[i]);
+        }
+    }
+};
+
+// kHalves: an item is the VEC elements at i and their partners at P + i, else
+// VEC consecutive elements (VEC / 2 pairs), two single ones in the form
+// without alignment (VEC == 1).
+template <typename T, int VEC, bool kHalves>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs p) {
+    constexpr bool kTwo = kHalves || VEC == 1;         // an item is two chunks
+    constexpr int kPairs = kTwo ? VEC : VEC / 2;       // pairs per item
+    constexpr int kHeads = kTwo ? 2 : 4;               // heads in flight per thread
+    extern __shared__ float2 table[];                  // [tokens][pairs] (cos, sin)
+    pdl_allow_next();
+    pdl_wait();
+    const int64_t m0 = static_cast<int64_t>(blockIdx.x) * p.tokens;
+    const int here = static_cast<int>(min(static_cast<int64_t>(p.tokens), p.M - m0));
+    for (int e = threadIdx.x; e < here * p.pairs; e += kRopeThreads) {
+        const int tok = e / p.pairs, i = e - tok * p.pairs;
+        const int64_t at = (m0 + tok) * p.pos_row_stride + p.axis[i] * p.pos_axis_stride;
+        const double pos = p.pos64 ? static_cast<double>(static_cast<const int64_t*>(p.pos)[at])
+                                   : static_cast<double>(static_cast<const int32_t*>(p.pos)[at]);
+        const double turns = pos * p.inv_turn[i];
+        float s, c;
+        sincospif(2.0f * static_cast<float>(turns - rint(turns)), &s, &c);
+        table[e] = make_float2(c, p.inverse ? -s : s);
+    }
+    __syncthreads();
+    const int heads = p.q.heads + p.k.heads;
+    const int per_token = p.items * p.head_lanes;
+    const int slot = threadIdx.x / per_token;
+    const int slots = kRopeThreads / per_token;
+    if (slot >= slots) return;
+    const int in_token = threadIdx.x - slot * per_token;
+    const int h0 = in_token / p.items;
+    const int item = in_token - h0 * p.items;
+    const bool rotates = item < p.rot_items;
+    // element offsets of the item's chunks within a head
+    int o0, o1;
+    if (!rotates) {
+        o0 = o1 = 2 * p.pairs + (item - p.rot_items) * VEC;
+    } else if constexpr (kHalves) {
+        o0 = item * VEC;
+        o1 = p.pairs + o0;
+    } else if constexpr (kTwo) {
+        o0 = 2 * item;
+        o1 = o0 + 1;
+    } else {
+        o0 = o1 = item * VEC;
+    }
+    for (int tok = slot; tok < here; tok += slots) {
+        float2 cs[kPairs];
+        if (rotates) {
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) cs[i] = table[tok * p.pairs + item * kPairs + i];
+        }
+        const int64_t m = m0 + tok;
+        for (int hb = h0; hb < heads; hb += kHeads * p.head_lanes) {
+            Chunk<T, VEC> a[kHeads], b[kTwo ? kHeads : 1];
+            T* out[kHeads];
+#pragma unroll
+            for (int j = 0; j < kHeads; ++j) {
+                const int h = hb + j * p.head_lanes;
+                if (h < heads) {
+                    const bool is_k = h >= p.q.heads;
+                    const RopeTensor& t = is_k ? p.k : p.q;
+                    const int hl = is_k ? h - p.q.heads : h;
+                    const T* in = static_cast<const T*>(t.in) + m * t.row_stride + hl * t.head_stride;
+                    out[j] = static_cast<T*>(t.out) + m * t.out_row_stride + hl * t.out_head_stride;
+                    a[j].load(in + o0);
+                    if constexpr (kTwo)
+                        if (rotates) b[j].load(in + o1);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kHeads; ++j) {
+                if (hb + j * p.head_lanes >= heads) continue;
+                if (rotates) {
+                    float fa[VEC];
+                    a[j].get(fa);
+                    if constexpr (kTwo) {
+                        float fb[VEC];
+                        b[j].get(fb);
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) {
+                            const float x = fa[i], y = fb[i];
+                            fa[i] = fmaf(x, cs[i].x, -(y * cs[i].y));
+                            fb[i] = fmaf(x, cs[i].y, y * cs[i].x);
+                        }
+                        b[j].set(fb);
+                        b[j].store(out[j] + o1);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < kPairs; ++i) {
+                            const float x = fa[2 * i], y = fa[2 * i + 1];
+                            fa[2 * i] = fmaf(x, cs[i].x, -(y * cs[i].y));
+                            fa[2 * i + 1] = fmaf(x, cs[i].y, y * cs[i].x);
+                        }
+                    }
+                    a[j].set(fa);
+                }
+                a[j].store(out[j] + o0);
+            }
+        }
+    }
+}
+
+using RopeKernel = void (*)(const RopeArgs);
+
+template <typename T>
+RopeKernel rope_kernel_for(bool vec, bool halves) {
+    constexpr int V = 16 / sizeof(T);
+    if (vec) return halves ? rope_kernel<T, V, true> : rope_kernel<T, V, false>;
+    return halves ? rope_kernel<T, 1, true> : rope_kernel<T, 1, false>;
+}
+
+bool rope_aligned(const RopeTensor& t, int e) {
+    return t.heads == 0 || (aligned16(t.in) && aligned16(t.out) && t.row_stride * e % 16 == 0 &&
+                            t.head_stride * e % 16 == 0 && t.out_row_stride * e % 16 == 0 &&
+                            t.out_head_stride * e % 16 == 0);
+}
+
+}  // namespace
+
+tfq_status launch_rope(const RopeTensor& q, const RopeTensor& k, int64_t M, int D, int dtype, const void* pos,
+                       bool pos64, int64_t pos_row_stride, int64_t pos_axis_stride, int pairs, const double* inv_freq,
+                       const int32_t* axis, bool halves, bool inverse, cudaStream_t stream) {
+    const int heads = q.heads + k.heads;
+    const int e = dtype == TFQ_DTYPE_FP32 ? 4 : 2;
+    const int V = 16 / e;
+    // 16-byte accesses need aligned heads whose rotated part (each half of it
+    // in the halves pairing) and copied part are whole units
+    const bool vec = rope_aligned(q, e) && rope_aligned(k, e) && D % V == 0 &&
+                     (halves ? pairs % V == 0 : 2 * pairs % V == 0);
+    RopeArgs a = {};
+    a.q = q;
+    a.k = k;
+    a.M = M;
+    a.D = D;
+    a.pairs = pairs;
+    a.rot_items = vec ? (halves ? pairs / V : 2 * pairs / V) : pairs;
+    a.items = a.rot_items + (D - 2 * pairs) / (vec ? V : 1);
+    a.head_lanes = std::max(1, std::min(heads, kRopeThreads / a.items));
+    a.inverse = inverse;
+    a.pos = pos;
+    a.pos64 = pos64;
+    a.pos_row_stride = pos_row_stride;
+    a.pos_axis_stride = pos_axis_stride;
+    constexpr double kInvTwoPi = 0.15915494309189533577;  // 1 / (2 pi)
+    for (int i = 0; i < pairs; ++i) {
+        a.inv_turn[i] = inv_freq[i] * kInvTwoPi;
+        a.axis[i] = static_cast<uint8_t>(axis[i]);
+    }
+    // tokens per CTA: a table entry or more for every thread, and work for every token slot
+    const int slots = kRopeThreads / (a.items * a.head_lanes);
+    const int table_tokens = std::max(1, kRopeThreads / std::max(1, pairs));
+    a.tokens = static_cast<int>(std::min<int64_t>(M, std::max(slots, table_tokens)));
+    const size_t smem = static_cast<size_t>(a.tokens) * pairs * sizeof(float2);
+    const int64_t blocks = (M + a.tokens - 1) / a.tokens;
+    auto kernel = dtype == TFQ_DTYPE_FP32   ? rope_kernel_for<float>(vec, halves)
+                  : dtype == TFQ_DTYPE_FP16 ? rope_kernel_for<__half>(vec, halves)
+                                            : rope_kernel_for<__nv_bfloat16>(vec, halves);
+    cudaError_t err = launch_kernel(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kRopeThreads), smem, stream, a);
+    if (err == cudaSuccess) err = cudaGetLastError();
+    return err == cudaSuccess ? TFQ_OK : fail(TFQ_ECUDA, "rotary launch: %s", cudaGetErrorString(err));
+}
+
+}  // namespace tfq

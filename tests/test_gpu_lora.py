@@ -1,0 +1,159 @@
+"""The scaled FP8 Linear with low-rank adapters on the GPU, against the formula
+in 64 bits (the codes' exact products, lora_Bs as the call is given it).
+
+Tolerance: that of the scaled GEMM (2^-7 |y| + 1e-3 rms(y)), which covers the
+fp32 sum over K and the output's rounding, plus the adapters': the rank-R
+intermediate is rounded to bf16 (half a step: 2^-8 relative) and carries the
+rounding of an fp32 sum of K products (K 2^-24 of the sum of their magnitudes).
+"""
+import pytest
+import torch
+
+import int8_w8a8_quantized_b200 as tfq
+from int8_w8a8_quantized_b200 import build
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build.build()
+
+
+def problem(M, N, K, R, n, order, bias, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed + M + N + K + R)
+    x = torch.randn((M, K), generator=g, device="cuda").bfloat16()
+    w = (0.05 * torch.randn((N, K), generator=g, device="cuda")).bfloat16()
+    A_q, s_a = tfq.tfq_quant_act_fp8_per_token(x)
+    W_q, s_w = tfq.tfq_quant_weight_per_channel(w)
+    A = (torch.randn((n, R, K), generator=g, device="cuda") / K ** 0.5).bfloat16()
+    B = torch.randn((n, N, R), generator=g, device="cuda").bfloat16()
+    scaling = torch.rand(n, generator=g, device="cuda") + 0.5
+    if order == "runs":
+        idx = torch.sort(torch.randint(-1, n, (M,), generator=g, device="cuda")).values
+    elif order == "any":
+        idx = torch.randint(-1, n, (M,), generator=g, device="cuda")
+    elif order == "none":
+        idx = torch.full((M,), -1, device="cuda")
+    elif order == "wild":  # values outside [0, n) mean no adapter
+        idx = torch.randint(-3, n + 3, (M,), generator=g, device="cuda")
+        idx[::5], idx[1::7] = -2 ** 31, 2 ** 31 - 1
+    else:
+        idx = torch.full((M,), n - 1, device="cuda")
+    b = torch.randn(N, generator=g, device="cuda").bfloat16() if bias else None
+    return dict(A_q=A_q, s_a=s_a, W_q=W_q, s_w=s_w, x=x, lora_A=A, lora_Bs=tfq.tfq_lora_fold(B, scaling, s_w),
+                adapter=idx.to(torch.int32), bias=b)
+
+
+def e4m3(q):
+    return q.view(torch.float8_e4m3fn).double()
+
+
+def check(p, y):
+    base = (e4m3(p["A_q"]) * p["s_a"].double()[:, None]) @ (e4m3(p["W_q"]) * p["s_w"].double()[:, None]).t()
+    if p["bias"] is not None:
+        base = base + p["bias"].double()
+    n, K = p["lora_A"].shape[0], p["x"].shape[1]
+    ref, tol = base.clone(), torch.zeros_like(base)
+    for a in range(n):
+        rows = torch.nonzero(p["adapter"] == a).flatten()
+        if rows.numel() == 0:
+            continue
+        x, A = p["x"][rows].double(), p["lora_A"][a].double()
+        B = p["lora_Bs"][a].double() * p["s_w"].double()[:, None]
+        t = x @ A.t()
+        ref[rows] += t @ B.t()
+        tol[rows] = (t.abs() * 2.0 ** -8 + (K * 2.0 ** -24) * (x.abs() @ A.abs().t())) @ B.abs().t() * 1.01
+    tol += 2.0 ** -7 * ref.abs() + 1e-3 * ref.square().mean().sqrt()
+    err = (y.double() - ref).abs()
+    assert torch.isfinite(y).all()
+    assert (err <= tol).all(), f"worst error / tolerance {float((err / tol).max()):.3f}"
+
+
+CASES = [  # M, N, K, R, adapters
+    (1, 8, 16, 8, 1), (1, 5120, 5120, 16, 3), (2, 136, 144, 24, 2), (7, 264, 1040, 32, 7), (16, 512, 256, 64, 40),
+    (64, 1024, 2064, 16, 64), (65, 1000, 528, 40, 5), (128, 256, 512, 128, 3), (129, 264, 272, 8, 200),
+    (300, 520, 1024, 256, 4), (511, 328, 784, 72, 6), (512, 256, 512, 64, 2), (600, 1032, 528, 16, 9),
+    (1025, 776, 2064, 64, 33), (2500, 520, 1040, 200, 5), (4111, 264, 272, 24, 100),
+]
+
+
+@pytest.mark.parametrize("order", ["runs", "any", "one"])
+@pytest.mark.parametrize("M,N,K,R,n", CASES)
+def test_lora(M, N, K, R, n, order):
+    p = problem(M, N, K, R, n, order, bias=bool(M % 2))
+    out = torch.full((M * N + 64,), 3.0, device="cuda", dtype=torch.bfloat16)
+    y = tfq.tfq_scaled_fp8_linear_lora(**p, out=out[:M * N].view(M, N))
+    tfq.tfq_device_error()
+    assert (out[M * N:] == 3).all()
+    check(p, y)
+
+
+@pytest.mark.parametrize("M", [5, 200, 700])
+def test_rows_without_an_adapter(M):
+    """No adapter: the plain Linear's value; indexes outside [0, n) of any size read nothing."""
+    p = problem(M, 264, 272, 16, 3, "none", True)
+    y = tfq.tfq_scaled_fp8_linear_lora(**p)
+    check(p, y)
+    p = problem(M, 264, 272, 16, 3, "wild", True)
+    check(p, tfq.tfq_scaled_fp8_linear_lora(**p))
+
+
+def test_no_adapters_is_the_plain_linear():
+    p = problem(300, 264, 272, 16, 3, "any", True)
+    want = tfq.tfq_scaled_fp8_linear(p["A_q"], p["s_a"], p["W_q"], p["s_w"], p["bias"])
+    p["lora_A"], p["lora_Bs"] = p["lora_A"][:0], p["lora_Bs"][:0]
+    assert torch.equal(tfq.tfq_scaled_fp8_linear_lora(**p), want)
+
+
+def test_stale_workspace_and_rows_of_other_calls():
+    """The workspace's contents mean nothing: NaN everywhere before the call, and the same bits after."""
+    for M in (3, 130, 777):
+        p = problem(M, 264, 528, 24, 4, "any", False)
+        n = tfq.tfq_scaled_fp8_linear_lora_workspace_bytes(M, 24)
+        ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+        y = tfq.tfq_scaled_fp8_linear_lora(**p, workspace=ws)
+        check(p, y)
+        again = tfq.tfq_scaled_fp8_linear_lora(**p, workspace=ws)
+        assert torch.equal(y, again)
+
+
+def test_zero_rows_and_channels():
+    """All-zero activations (scale at its floor) and all-zero weight channels: only bias and adapters are left."""
+    p = problem(140, 264, 272, 16, 2, "one", True)
+    x = p["x"].clone()
+    x[::3] = 0
+    p["x"] = x
+    p["A_q"], p["s_a"] = tfq.tfq_quant_act_fp8_per_token(x)
+    y = tfq.tfq_scaled_fp8_linear_lora(**p)
+    check(p, y)
+    assert torch.equal(y[0], p["bias"])
+
+
+def test_fold():
+    g = torch.Generator(device="cuda").manual_seed(0)
+    for n, N, R in ((1, 1, 1), (3, 40, 7), (5, 264, 64)):
+        B = torch.randn((n, N, R), generator=g, device="cuda").bfloat16()
+        s = torch.rand(n, generator=g, device="cuda") + 0.5
+        w = torch.rand(N, generator=g, device="cuda") * 1e-3 + 1e-5
+        got = tfq.tfq_lora_fold(B, s, w)
+        want = ((B.float() * s[:, None, None]) / w[None, :, None]).bfloat16()
+        assert torch.equal(got, want)
+        assert torch.equal(tfq.tfq_lora_fold(B, None, w), (B.float() / w[None, :, None]).bfloat16())
+        tfq.tfq_lora_fold(B, s, w, out=B)
+        assert torch.equal(B, want)
+
+
+def test_refused_calls():
+    p = problem(4, 16, 32, 8, 2, "any", False)
+    for k, v in (("x", p["x"].float()), ("x", p["x"][:3]), ("lora_A", p["lora_A"][:, :, :16]),
+                 ("lora_Bs", p["lora_Bs"][:1]), ("adapter", p["adapter"].long()), ("adapter", p["adapter"][:2]),
+                 ("s_a", p["s_a"].cpu()), ("A_q", p["A_q"].to(torch.int8))):
+        with pytest.raises((TypeError, ValueError)):
+            tfq.tfq_scaled_fp8_linear_lora(**{**p, k: v})
+    with pytest.raises(ValueError, match="workspace"):
+        tfq.tfq_scaled_fp8_linear_lora(**p, workspace=torch.empty(1, dtype=torch.uint8, device="cuda"))
+    p = problem(4, 16, 32, 16, 2, "any", False)
+    with pytest.raises(tfq.TfqError):
+        tfq.tfq_scaled_fp8_linear_lora(**{**p, "lora_A": p["lora_A"][:, :12].contiguous(),
+                                          "lora_Bs": p["lora_Bs"][..., :12].contiguous()})

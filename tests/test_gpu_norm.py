@@ -1,0 +1,300 @@
+"""Layer norm on the GPU: forward, straight to FP8 codes, and gradients, against
+the formulas in 64 bits.
+
+Tolerances.  u = 2^-24 (an fp32 rounding).  A row's sums add at most 64
+elements in a thread, 5 shuffle steps, 32 warps: under 100 roundings, so the
+mean is off by at most 100 u mean|x|, the variance and hence rstd by 100 u
+relative (the terms are squares), and
+    d_xhat = 100 u (rstd mean|x| + |xhat|)
+bounds xhat's error.  The affine part adds 4 u of each term, the output
+rounding half a step of its type (eps / 2), 2^-25 absolute where fp16 is
+subnormal.
+"""
+import numpy as np
+import pytest
+import torch
+
+import int8_w8a8_quantized_b200 as tfq
+from int8_w8a8_quantized_b200 import _capi, build
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build.build()
+
+
+def half_step(v, dtype):
+    """Largest rounding error of a value v stored as dtype."""
+    if dtype == torch.float32:
+        return v.abs() * U + 2.0 ** -150
+    return v.abs() * (torch.finfo(dtype).eps / 2) + (2.0 ** -25 if dtype == torch.float16 else 0.0)
+
+
+def states(M, K, dtype, pad=0, seed=0, shift=0.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn((M, K + pad), generator=g, device="cuda") + shift
+    x[:, : max(1, K // 50)] *= 30
+    return x.to(dtype)[:, :K], g
+
+
+def affine(G, K, wdtype, g, which, two_d):
+    shape = (G, K) if two_d else (K,)
+    w = (1 + 0.3 * torch.randn(shape, generator=g, device="cuda")).to(wdtype) if which != "none" else None
+    b = (0.3 * torch.randn(shape, generator=g, device="cuda")).to(wdtype) if which == "both" else None
+    return w, b
+
+
+def spread(v, M, K):
+    v = v.double().reshape(-1, K)
+    return v.repeat_interleave(max(1, M // v.shape[0]), 0)[:M] if v.shape[0] > 1 else v.expand(M, K)
+
+
+def reference(x, w, b, eps, offset):
+    """(y, its error bound before the output rounding, xhat, d_xhat, rstd, mean), 64 bits."""
+    M, K = x.shape
+    x = x.double()
+    mean = x.mean(1, keepdim=True)
+    rstd = 1 / torch.sqrt(((x - mean) ** 2).mean(1, keepdim=True) + eps)
+    xhat = (x - mean) * rstd
+    d = 100 * U * (rstd * x.abs().mean(1, keepdim=True) + xhat.abs())
+    y, e = xhat, d
+    if w is not None:
+        wt = spread(w, M, K) + offset
+        y, e = y * wt, e * wt.abs() + 4 * U * (y * wt).abs() + 2 * U * xhat.abs() * wt.abs()
+    if b is not None:
+        bt = spread(b, M, K)
+        y, e = y + bt, e + 4 * U * (y.abs() + bt.abs())
+    return y, e, xhat, d, rstd, mean
+
+
+def guard(shape, dtype, fill=77.0):
+    """A buffer with 64 guard elements behind it: (the view, the check)."""
+    n = int(np.prod(shape))
+    t = torch.full((n + 64,), fill, device="cuda").to(dtype)
+    return t[:n].view(shape), lambda: bool((t[n:].float() == fill).all())
+
+
+SHAPES = [(1, 1), (1, 16), (3, 8), (5, 7), (33, 64), (300, 128), (7, 130), (64, 512), (2, 1001), (130, 1024),
+          (9, 1536), (6, 2048), (5, 5120), (3, 8192), (3, 8200), (2, 12288), (2, 13824), (1, 32768), (2, 32767),
+          (1200, 96)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("M,K", SHAPES)
+def test_forward(M, K, dtype):
+    seed = M * 7 + K
+    pad = (0, 3, 8)[seed % 3]
+    which = ("both", "weight", "none", "both")[seed % 4]
+    wdt = DT[dtype] if seed % 2 else torch.float32
+    offset = float(seed % 2)
+    x, g = states(M, K, DT[dtype], pad, seed, shift=float(seed % 5))
+    w, b = affine(1, K, wdt, g, which, two_d=bool(seed % 2))
+    yb, ok = guard((M, K), DT[dtype])
+    y, mean, rstd = tfq.tfq_layer_norm(x, w, b, eps=1e-5, weight_offset=offset, stats=True, y=yb)
+    ref, e, xhat, d, r, mu = reference(x, w, b, 1e-5, offset)
+    assert ((y.double() - ref).abs() <= e + half_step(ref.abs() + e, y.dtype)).all()
+    assert ok()
+    assert ((mean.double() - mu[:, 0]).abs() <= 101 * U * x.double().abs().mean(1) + 2.0 ** -149).all()
+    assert ((rstd.double() - r[:, 0]).abs() <= 104 * U * r[:, 0]).all()
+    tfq.tfq_device_error()
+
+
+@pytest.mark.parametrize("M,K,G", [(12, 64, 3), (40, 1001, 5), (64, 5120, 4), (6, 96, 6), (600, 256, 2), (2000, 128, 2)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_groups_equal_separate_calls(M, K, G, dtype):
+    x, g = states(M, K, DT[dtype], 0, K)
+    w, b = affine(G, K, torch.float32, g, "both", True)
+    y = tfq.tfq_layer_norm(x, w, b, weight_offset=1.0)
+    q, s = (tfq.tfq_layer_norm_quant_fp8(x, w, b, weight_offset=1.0) if K % 16 == 0 else (None, None))
+    n = M // G
+    for i in range(G):
+        rows = slice(i * n, (i + 1) * n)
+        # a group's rows start wherever they start: the same kernel, or the element form, whose sums run in another order
+        part = tfq.tfq_layer_norm(x[rows].contiguous(), w[i].contiguous(), b[i].contiguous(), weight_offset=1.0)
+        assert torch.equal(part, y[rows])
+        if q is not None:
+            pq, ps = tfq.tfq_layer_norm_quant_fp8(x[rows].contiguous(), w[i].contiguous(), b[i].contiguous(),
+                                                  weight_offset=1.0)
+            assert torch.equal(pq, q[rows]) and torch.equal(ps, s[rows])
+
+
+def e4m3_spacing(v):
+    """Distance of the E4M3 values around |v|."""
+    e = torch.floor(torch.log2(v.abs().clamp_min(2.0 ** -6)))
+    return torch.exp2(e - 3)
+
+
+@pytest.mark.parametrize("qmax", [448.0, 14.0, 7.0, 100.3])
+@pytest.mark.parametrize("M,K,dtype", [(1, 16, "bf16"), (37, 64, "fp16"), (9, 144, "fp32"), (70, 1024, "bf16"),
+                                       (5, 5120, "bf16"), (4, 5120, "fp32"), (3, 13824, "bf16"), (2, 32768, "bf16"),
+                                       (2, 32768, "fp32"), (600, 256, "bf16")])
+def test_quant(M, K, dtype, qmax):
+    seed = M + K
+    pad = (0, 3, 8)[seed % 3]
+    x, g = states(M, K, DT[dtype], pad, seed, shift=1.0)
+    which = ("both", "none", "weight")[seed % 3]
+    w, b = affine(1, K, torch.float32 if seed % 2 else DT[dtype], g, which, False)
+    qb, ok_q = guard((M, K), torch.uint8)
+    sb, ok_s = guard((M,), torch.float32)
+    q, s = tfq.tfq_layer_norm_quant_fp8(x, w, b, eps=1e-6, weight_offset=1.0, qmax=qmax, q=qb, s=sb)
+    assert ok_q() and ok_s()
+    ref, e, *_ = reference(x, w, b, 1e-6, 1.0)
+    want = ref.abs().amax(1).clamp_min(1e-12) / qmax
+    assert ((s.double() - want).abs() <= e.amax(1) / qmax + 2 * U * want).all()
+    t = ref / s.double()[:, None]
+    dt = e / s.double()[:, None] + 4 * U * t.abs()
+    v = q.view(torch.float8_e4m3fn).double()
+    # half the spacing of the binade that |t| + dt reaches; qmax that is no E4M3 value is clamped before the cast
+    assert ((v - t).abs() <= e4m3_spacing(t.abs() + dt) / 2 + dt).all()
+    assert not torch.isnan(v).any()
+
+
+def test_quant_constant_and_zero_rows():
+    x = torch.full((4, 64), 3.25, device="cuda", dtype=torch.bfloat16)
+    x[1] = 0
+    q, s = tfq.tfq_layer_norm_quant_fp8(x, None, None, eps=1e-6)
+    assert (q.view(torch.float8_e4m3fn).float() == 0).all()
+    assert torch.equal(s.cpu(), torch.full((4,), np.float32(np.float32(1e-12) / np.float32(448.0)).item()))
+    y = tfq.tfq_layer_norm(x, None, torch.arange(64, device="cuda").bfloat16())
+    assert torch.equal(y, torch.arange(64, device="cuda").bfloat16().expand(4, 64))
+
+
+def test_nonfinite_rows_stay_alone():
+    x, _ = states(6, 5120, torch.bfloat16, 0, 1)
+    x = x.contiguous()
+    clean = tfq.tfq_layer_norm(x)
+    x[1, 5], x[4, 9] = float("nan"), float("inf")
+    y = tfq.tfq_layer_norm(x)
+    for r in (0, 2, 3, 5):
+        assert torch.equal(y[r], clean[r])
+    assert torch.isnan(y[1]).all() and torch.isnan(y[4]).any()
+
+
+def test_large_offset_keeps_its_digits():
+    """mean 1000, deviation 1: summing squares would lose 2e4 of 1.7e7; x - mean does not."""
+    x = (1000 + torch.randn(8, 4096, device="cuda", generator=torch.Generator(device="cuda").manual_seed(0)))
+    y = tfq.tfq_layer_norm(x)
+    ref, e, *_ = reference(x, None, None, 1e-6, 0.0)
+    assert ((y.double() - ref).abs() <= e + half_step(ref, y.dtype)).all()
+    assert float((y.double() - ref).abs().max()) < 2e-3  # 100 u * 1000 is 6e-3; the sums do better
+
+
+BWD_SHAPES = [(1, 1, 1), (1, 16, 1), (6, 8, 3), (5, 7, 1), (33, 64, 1), (300, 128, 2), (7, 130, 1), (700, 512, 1),
+              (2, 1001, 1), (517, 1001, 1), (130, 1024, 1), (40, 1536, 4), (900, 5120, 3), (3, 8200, 1),
+              (4, 13824, 2), (2, 32768, 1), (2, 32767, 1), (1500, 96, 1), (12, 48, 12), (1300, 2048, 1)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("M,K,G", BWD_SHAPES)
+def test_backward(M, K, G, dtype):
+    seed = M * 3 + K
+    pad = (0, 3, 8)[seed % 3]
+    which = ("both", "weight", "none")[seed % 3]
+    wdt = DT[dtype] if seed % 2 else torch.float32
+    offset = float(seed % 2)
+    x, g = states(M, K, DT[dtype], pad, seed, shift=0.5)
+    w, b = affine(G, K, wdt, g, which, G > 1)
+    dy = torch.randn((M, K + pad), generator=g, device="cuda").to(DT[dtype])[:, :K]
+    _, mean, rstd = tfq.tfq_layer_norm(x, w, b, eps=1e-5, weight_offset=offset, stats=True)
+    dx, dw, db = tfq.tfq_layer_norm_backward(dy, x, w, mean, rstd, weight_offset=offset,
+                                             groups=None if w is not None else G)
+    tfq.tfq_device_error()
+    _, _, xhat, d, r, _ = reference(x, None, None, 1e-5, 0.0)
+    y64 = dy.double()
+    wt = spread(w, M, K) + offset if w is not None else torch.ones_like(y64)
+    h = y64 * wt
+    c1, c2 = h.mean(1, keepdim=True), (h * xhat).mean(1, keepdim=True)
+    ref = r * (h - c1 - xhat * c2)
+    dh = 2 * U * h.abs()
+    dc1 = 100 * U * h.abs().mean(1, keepdim=True)
+    dc2 = 100 * U * (h * xhat).abs().mean(1, keepdim=True) + (h.abs() * d).mean(1, keepdim=True)
+    e = r * (dh + dc1 + xhat.abs() * dc2 + d * (c2.abs() + dc2) + 4 * U * (h.abs() + c1.abs() + (xhat * c2).abs()))
+    e = e + 110 * U * ref.abs()
+    assert ((dx.double() - ref).abs() <= e + half_step(ref.abs() + e, dx.dtype)).all()
+    n = M // G
+    groups = lambda v: v.view(G, n, K)  # noqa: E731
+    adds = n + 16
+    if w is not None:
+        rw = groups(y64 * xhat).sum(1)
+        ew = groups(y64.abs() * d + adds * U * (y64 * xhat).abs()).sum(1)
+        assert ((dw.double().view(G, K) - rw).abs() <= ew + half_step(rw.abs() + ew, dw.dtype)).all()
+        assert dw.dtype == w.dtype and dw.shape == w.shape
+    else:
+        assert dw is None
+    rb = groups(y64).sum(1)
+    eb = adds * U * groups(y64.abs()).sum(1)
+    assert ((db.double().view(G, K) - rb).abs() <= eb + half_step(rb.abs() + eb, db.dtype)).all()
+
+
+def test_backward_against_differences():
+    """dx, dw and db against central differences of the 64-bit forward's sum(y * dy)."""
+    M, K = 3, 24
+    x, g = states(M, K, torch.float32, 0, 5)
+    w, b = affine(1, K, torch.float32, g, "both", False)
+    dy = torch.randn((M, K), generator=g, device="cuda")
+    _, mean, rstd = tfq.tfq_layer_norm(x, w, b, eps=1e-3, stats=True)
+    dx, dw, db = tfq.tfq_layer_norm_backward(dy, x, w, mean, rstd)
+
+    def loss(x, w, b):
+        mu = x.mean(1, keepdim=True)
+        xh = (x - mu) / torch.sqrt(((x - mu) ** 2).mean(1, keepdim=True) + 1e-3)
+        return float(((xh * w + b) * dy.double()).sum())
+
+    args = [x.double(), w.double(), b.double()]
+    h = 1e-5  # truncation h^2 f''' ~ 1e-10, rounding 1e-16 / h ~ 1e-11; fp32 results carry 1e-5 of the largest term
+    for t, grad in zip(range(3), (dx, dw, db)):
+        flat = grad.double().flatten()
+        for i in range(0, flat.numel(), 5):
+            lo, hi = [a.clone() for a in args], [a.clone() for a in args]
+            lo[t].view(-1)[i] -= h
+            hi[t].view(-1)[i] += h
+            diff = (loss(*hi) - loss(*lo)) / (2 * h)
+            assert abs(diff - float(flat[i])) <= 1e-5 * (1 + float(flat.abs().max()))
+
+
+def test_backward_parts_and_broadcast_inputs():
+    """Each gradient alone equals the one of the full call; an expanded dy (row stride 0) is refused."""
+    x, g = states(200, 768, torch.bfloat16, 0, 3)
+    x = x.contiguous()
+    w, b = affine(1, 768, torch.float32, g, "both", False)
+    dy = torch.randn(200, 768, generator=g, device="cuda").bfloat16()
+    _, mean, rstd = tfq.tfq_layer_norm(x, w, b, stats=True)
+    full = tfq.tfq_layer_norm_backward(dy, x, w, mean, rstd)
+    again = tfq.tfq_layer_norm_backward(dy, x, w, mean, rstd)
+    assert all(torch.equal(a, c) for a, c in zip(full, again))  # the same bits
+    for i in range(3):
+        need = dict(need_x=i == 0, need_weight=i == 1, need_bias=i == 2)
+        part = tfq.tfq_layer_norm_backward(dy, x, w, mean, rstd, **need)
+        assert [p is None for p in part] == [j != i for j in range(3)]
+        assert torch.equal(part[i], full[i])
+    with pytest.raises(ValueError, match="overlap"):
+        tfq.tfq_layer_norm_backward(dy[:1].expand(200, 768), x, w, mean, rstd)
+
+
+def test_empty_and_refused_calls():
+    e = torch.empty((0, 64), device="cuda", dtype=torch.bfloat16)
+    w = torch.ones(64, device="cuda")
+    y, mean, rstd = tfq.tfq_layer_norm(e, w, w, stats=True)
+    assert y.shape == (0, 64) and mean.shape == (0,)
+    dx, dw, db = tfq.tfq_layer_norm_backward(e, e, w, mean, rstd)
+    assert dx.shape == (0, 64) and (dw == 0).all() and (db == 0).all()
+    assert tfq.tfq_layer_norm(torch.empty((3, 0), device="cuda")).shape == (3, 0)
+    q, s = tfq.tfq_layer_norm_quant_fp8(torch.empty((3, 0), device="cuda"))
+    assert q.shape == (3, 0) and (s > 0).all()
+    x = torch.zeros(4, 64, device="cuda")
+    for bad in (dict(weight=torch.ones(63, device="cuda")), dict(weight=w.double()), dict(weight=w.cpu()),
+                dict(weight=torch.ones(3, 64, device="cuda")), dict(weight=w, bias=w.half())):
+        with pytest.raises((TypeError, ValueError)):
+            tfq.tfq_layer_norm(x, **bad)
+    with pytest.raises(ValueError, match="contiguous rows"):
+        tfq.tfq_layer_norm(x.t())
+    with pytest.raises(TypeError):
+        tfq.tfq_layer_norm(x.double())
+    with pytest.raises(tfq.TfqError):
+        tfq.tfq_layer_norm_quant_fp8(torch.zeros(2, 24, device="cuda"))
+    with pytest.raises(tfq.TfqError):
+        tfq.tfq_layer_norm(torch.zeros(1, _capi.TFQ_NORM_MAX_K + 1, device="cuda"))
