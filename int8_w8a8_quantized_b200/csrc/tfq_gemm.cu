@@ -40,6 +40,8 @@
 // Every wait is bounded (see tfq_ptx.cuh); a CTA that gives up records it in
 // the error word, drains its own outstanding copies and MMAs, frees TMEM and
 // returns.
+#include <type_traits>
+
 #include "tfq_gemm_common.cuh"
 #include "tfq_quant_row.cuh"
 
@@ -231,7 +233,8 @@ struct PairCfg {
     static constexpr int kTmemCols = 512;                       // two PBN-column accumulators, power of 2
     static constexpr size_t kRing = static_cast<size_t>(PAIR_STAGES) * (kAStage + kBStage);
     static constexpr size_t kSmem = 1024 + kRing + SMEM_EPI + (2 * PAIR_STAGES + 4 + 1) * 8 + 16;
-    static_assert(kSmem <= 232448, "shared memory budget exceeded");
+    static constexpr size_t kSmemLora = kSmem + 8 + 4 * PAIR_STAGES;  // one barrier, a word per stage
+    static_assert(kSmemLora <= 232448, "shared memory budget exceeded");
     static_assert(2 * PBN <= kTmemCols, "two accumulators must fit in TMEM");
     static_assert(PBN % 64 == 0 && PBN >= 64 && PBN <= 256, "N tile");
 };
@@ -341,9 +344,211 @@ struct LinearOperands {
     void* out;
 };
 
-template <int PBN, int kAcc, int kQuant = 0>
+// The CTA-pair kernel with low-rank adapters beside the Linear (kLora): row m
+// adds sum_r t[m,r] Bs[a,n,r], a = idx[m], to its accumulator, with t and Bs in
+// units of the row's and the column's scale (tfq_lora.cu), so the epilogue's
+// s_a s_w covers both sums.  A tile's accumulator starts with one kind::f16
+// step per adapter present in its 256 rows and 64 columns of the rank, then
+// takes the kind::f8f6f4 steps of the Linear.  For adapter a the A operand is
+// t with the rows of other adapters zero: one tiled load where every row of
+// the CTA's half belongs to a (or none does: a box past the end, all zero
+// fill), else a gather that takes the zero row t[M] for the others, four
+// rows per lane of the producer warp.  The adapters of a tile are enumerated
+// in increasing order from idx by both producers alike; the even one leaves
+// each stage's kind in shared memory for the MMA thread.  Between the two
+// kinds the MMA thread waits for the first: only instructions of one shape
+// are ordered among themselves.
+struct LoraPairMaps : PairMaps {
+    CUtensorMap t;    // t [M + 1, R] bf16, 64 x 128 boxes
+    CUtensorMap tg;   // the same, one-row boxes for the gather
+    CUtensorMap bs;   // Bs [n_adapters * N, R], 64 x PBN / 2 boxes
+    CUtensorMap bsq;  // ... 64 x PBN / 4 boxes (half-width tiles)
+    const int32_t* idx;
+    int n_adapters;
+    int R;
+};
+
+// A stage's contents, for the MMA thread.
+enum : uint32_t { kStageLora = 1u << 3, kStageFirst = 1u << 4, kStageLast = 1u << 5, kStageSteps = 7u };
+
+// idx[m] where it names an adapter, else 0xFFFFFFFF.
+__device__ __forceinline__ uint32_t row_adapter(const int32_t* idx, int m, int M, int n_adapters) {
+    if (m >= M) return 0xFFFFFFFFu;
+    const uint32_t a = static_cast<uint32_t>(__ldg(idx + m));
+    return a < static_cast<uint32_t>(n_adapters) ? a : 0xFFFFFFFFu;
+}
+
+template <int PBN>
+__device__ __forceinline__ void lora_pair_producer(const CUtensorMap& tmA, const LoraPairMaps& maps, const GemmArgs& p,
+                                                   uint8_t* sA, uint8_t* sB, uint64_t* full, uint64_t* empty,
+                                                   uint32_t* stage_info, volatile int* abort_flag, int rank,
+                                                   int cluster, int n_clusters, int lane) {
+    using C = PairCfg<PBN>;
+    const int m_tiles = (p.M + 255) / 256;
+    const int total_tiles = m_tiles * p.n_tiles;
+    const int r_chunks = (maps.R + 63) / 64;
+    uint64_t pol_a, pol_b;
+    l2_policies(p, pol_a, pol_b);
+    int it = 0;
+    int round = 0, t, half;
+    bool ok = true;
+    for (int w = cluster; ok && pair_work_item(w, total_tiles, n_clusters, p.tail_halves, t, half);
+         w += n_clusters, ++round) {
+        if (rank == 0 && lane == 0) pace_round(p.round_ctr, round, total_tiles, n_clusters);
+        __syncwarp();
+        int tm, tn;
+        pair_tile_coords(t, m_tiles, p.n_tiles, p.group_m, p.band_n, tm, tn);
+        const int b_rows = half < 0 ? C::kBHalf : C::kBHalf / 2;
+        const uint32_t stage_tx = 2 * static_cast<uint32_t>(C::kAStage + b_rows * BK);
+        const int a_row = tm * 256 + rank * 128;
+        const int b_row = tn * PBN + (half > 0 ? PBN / 2 : 0) + rank * b_rows;
+        const CUtensorMap* tmb = half < 0 ? &maps.b[0] : &maps.bq[0];
+        const CUtensorMap* tmbs = half < 0 ? &maps.bs : &maps.bsq;
+        // the adapters of the tile's rows (8 per lane) and of this CTA's half (4 per lane)
+        uint32_t all[8], mine[4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) all[i] = row_adapter(maps.idx, tm * 256 + lane * 8 + i, p.M, maps.n_adapters);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mine[i] = row_adapter(maps.idx, a_row + lane * 4 + i, p.M, maps.n_adapters);
+        uint32_t flags = kStageFirst;
+        uint32_t from = 0;  // adapters below are done
+        for (;;) {
+            uint32_t a = 0xFFFFFFFFu;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) a = min(a, all[i] >= from ? all[i] : 0xFFFFFFFFu);
+            a = __reduce_min_sync(0xFFFFFFFFu, a);
+            if (a == 0xFFFFFFFFu) break;
+            from = a + 1;
+            bool every = true, any = false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                any = any || mine[i] == a;
+                every = every && (mine[i] == a || a_row + lane * 4 + i >= p.M);
+            }
+            any = __any_sync(0xFFFFFFFFu, any);
+            every = __all_sync(0xFFFFFFFFu, every);
+            for (int c = 0; c < r_chunks; ++c, ++it) {
+                const int st = it % PAIR_STAGES;
+                const uint32_t ph = static_cast<uint32_t>(it / PAIR_STAGES) & 1u;
+                if (lane == 0) ok = mbar_wait(&empty[st], ph ^ 1u, abort_flag);
+                ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
+                if (!ok) break;
+                __syncwarp();  // every lane's copies come after the stage was found free
+                const uint32_t full_leader = mapa_shared(smem_u32(&full[st]), 0);
+                uint8_t* dst = sA + st * C::kAStage;
+                if (lane == 0) {
+                    if (rank == 0) {
+                        stage_info[st] = flags | kStageLora | static_cast<uint32_t>(min(4, (maps.R - c * 64 + 15) / 16));
+                        mbar_arrive_expect_tx(&full[st], stage_tx);
+                    }
+                    tma_load_2d_pair(sB + st * C::kBStage, tmbs, c * 64, static_cast<int>(a) * p.N + b_row,
+                                     full_leader, pol_b);
+                    // all rows or none: one box, the latter past the last row of t
+                    if (every || !any)
+                        tma_load_2d_pair(dst, &maps.t, c * 64, any ? a_row : p.M + 1, full_leader, pol_a);
+                }
+                if (any && !every)
+                    tma_gather4_pair(dst + lane * 512, &maps.tg, c * 64, mine[0] == a ? a_row + lane * 4 : p.M,
+                                     mine[1] == a ? a_row + lane * 4 + 1 : p.M,
+                                     mine[2] == a ? a_row + lane * 4 + 2 : p.M,
+                                     mine[3] == a ? a_row + lane * 4 + 3 : p.M, full_leader);
+                flags = 0;
+                __syncwarp();
+            }
+            if (!ok) break;
+        }
+        if (lane == 0) {
+            for (int kb = 0; ok && kb < p.k_blocks; ++kb, ++it) {
+                const int st = it % PAIR_STAGES;
+                const uint32_t ph = static_cast<uint32_t>(it / PAIR_STAGES) & 1u;
+                ok = mbar_wait(&empty[st], ph ^ 1u, abort_flag);
+                if (!ok) break;
+                const uint32_t full_leader = mapa_shared(smem_u32(&full[st]), 0);
+                if (rank == 0) {
+                    stage_info[st] = flags | static_cast<uint32_t>(BK / UMMA_K) | (kb == p.k_blocks - 1 ? kStageLast : 0u);
+                    mbar_arrive_expect_tx(&full[st], stage_tx);
+                }
+                tma_load_2d_pair(sA + st * C::kAStage, &tmA, kb * BK, a_row, full_leader, pol_a);
+                tma_load_2d_pair(sB + st * C::kBStage, tmb, kb * BK, b_row, full_leader, pol_b);
+                flags = 0;
+            }
+            if (ok && rank == 0 && p.round_ctr != nullptr) atomicAdd(p.round_ctr, 1u);
+        }
+        ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
+        it = __shfl_sync(0xFFFFFFFFu, it, 0);
+    }
+    if (lane != 0) return;
+    if (!ok) give_up(abort_flag, p.err, kErrGemmProducer);
+    // As in the plain producer: the even CTA's waits out every load in flight.
+    if (rank == 0) {
+        for (int i = max(0, it - PAIR_STAGES); i < it; ++i)
+            if (!mbar_wait(&full[i % PAIR_STAGES], static_cast<uint32_t>(i / PAIR_STAGES) & 1u, nullptr))
+                atomicOr(p.err, kErrGemmDrain);
+        pacing_done(p.round_ctr, n_clusters);
+    }
+}
+
+// The MMA thread of the even CTA: stages as their kind says (see above).
+template <int PBN>
+__device__ __forceinline__ void lora_pair_mma(const GemmArgs& p, uint8_t* sA, uint8_t* sB, uint64_t* full,
+                                              uint64_t* empty, uint64_t* tmem_full, uint64_t* tmem_empty,
+                                              uint64_t* order, const volatile uint32_t* stage_info,
+                                              volatile int* abort_flag, uint32_t tmem_base, int cluster,
+                                              int n_clusters) {
+    using C = PairCfg<PBN>;
+    const int total_tiles = (p.M + 255) / 256 * p.n_tiles;
+    int it = 0, tcount = 0, t, half;
+    uint32_t order_phase = 0;
+    bool ok = true;
+    for (int w = cluster; ok && pair_work_item(w, total_tiles, n_clusters, p.tail_halves, t, half);
+         w += n_clusters, ++tcount) {
+        const int buf = tcount & 1;
+        const uint32_t use = static_cast<uint32_t>(tcount >> 1);
+        ok = mbar_wait(&tmem_empty[buf], (use & 1u) ^ 1u, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        const int n = half < 0 ? PBN : PBN / 2;
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * PBN);
+        uint32_t info = 0;
+        do {
+            const int st = it % PAIR_STAGES;
+            ok = mbar_wait(&full[st], static_cast<uint32_t>(it / PAIR_STAGES) & 1u, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            const bool was_lora = (info & kStageLora) != 0;
+            info = stage_info[st];
+            if (was_lora && (info & kStageLora) == 0) {
+                mma_commit_pair(order, 0x1);
+                ok = mbar_wait(order, order_phase, abort_flag);
+                if (!ok) break;
+                order_phase ^= 1u;
+                tc_fence_after();
+            }
+            const uint64_t a_desc = sw128_kmajor_desc(sA + st * C::kAStage);
+            const uint64_t b_desc = sw128_kmajor_desc(sB + st * C::kBStage);
+            uint32_t acc = (info & kStageFirst) != 0 ? 0u : 1u;
+            if ((info & kStageLora) != 0) {
+                const uint32_t idesc = make_idesc_bf16(256, n);
+                for (uint32_t k = 0; k < (info & kStageSteps); ++k, acc = 1u)
+                    mma_bf16_pair(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc, acc);
+            } else {
+                const uint32_t idesc = make_idesc<kAccF32>(256, n);
+#pragma unroll
+                for (int k = 0; k < BK / UMMA_K; ++k, acc = 1u)
+                    mma_e4m3_pair<false>(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc, acc);
+            }
+            mma_commit_pair(&empty[st], 0x3);
+            ++it;
+        } while ((info & kStageLast) == 0);
+        if (ok) mma_commit_pair(&tmem_full[buf], 0x3);
+    }
+    if (!ok) give_up(abort_flag, p.err, kErrGemmMma);
+}
+
+template <int PBN, int kAcc, int kQuant = 0, bool kLora = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads<kQuant>(), 1)
-    scaled_mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ PairMaps maps,
+    scaled_mm_pair_kernel(const __grid_constant__ CUtensorMap tmA,
+                          const __grid_constant__ std::conditional_t<kLora, LoraPairMaps, PairMaps> maps,
                           GemmArgs p) {
     using C = PairCfg<PBN>;
     extern __shared__ uint8_t smem_raw[];
@@ -358,6 +563,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads<kQuant>
     uint64_t* drain = tmem_empty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    // kLora only (the last 16 bytes hold the two words above)
+    uint64_t* order = drain + 3;
+    uint32_t* stage_info = reinterpret_cast<uint32_t*>(order + 1);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -377,6 +585,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads<kQuant>
             mbar_init(&tmem_empty[i], 2 * EPI_WARPS);
         }
         mbar_init(drain, 1);
+        if constexpr (kLora) mbar_init(order, 1);
         *abort_flag = 0;
         fence_mbar_init();
         prefetch_tensormap(&tmA);
@@ -399,7 +608,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads<kQuant>
 
     if (warp == 0) {
         // ---------------------------------------------------- TMA producer
-        if (lane == 0) {
+        if constexpr (kLora) {
+            lora_pair_producer<PBN>(tmA, maps, p, sA, sB, full, empty, stage_info, abort_flag, static_cast<int>(rank),
+                                    cluster, n_clusters, lane);
+        } else if (lane == 0) {
             uint64_t pol_a, pol_b;
             l2_policies(p, pol_a, pol_b);
             int it = 0;
@@ -455,7 +667,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads<kQuant>
         }
     } else if (warp == 1) {
         // ------------------------------------------- MMA issuer (even CTA)
-        if (lane == 0 && rank == 0) {
+        if constexpr (kLora) {
+            if (lane == 0 && rank == 0) {
+                lora_pair_mma<PBN>(p, sA, sB, full, empty, tmem_full, tmem_empty, order, stage_info, abort_flag,
+                                   tmem_base, cluster, n_clusters);
+                mma_commit_pair(drain, 0x1);
+                if (!mbar_wait(drain, 0, nullptr)) atomicOr(p.err, kErrGemmDrain);
+            }
+        } else if (lane == 0 && rank == 0) {
             int it = 0, tcount = 0, t, half;
             bool ok = true;
             for (int w = cluster; ok && pair_work_item(w, total_tiles, n_clusters, p.tail_halves, t, half);
@@ -805,6 +1024,57 @@ tfq_status launch_gemm_multi(const void* A, const float* s_a, int64_t M, int64_t
 }
 
 }  // namespace
+
+// The Linear with the adapters' rows t [M + 1, R] (row M zero) beside it.
+tfq_status launch_lora_pair_gemm(const void* A, const float* s_a, const void* W, const float* s_w, const void* bias,
+                                 int64_t M, int64_t N, int64_t K, const LoraCall& l, const void* t, void* out,
+                                 cudaStream_t stream, DeviceState* ds) {
+    constexpr int kPBN = 256;
+    using C = PairCfg<kPBN>;
+    auto kernel = scaled_mm_pair_kernel<kPBN, kAccF32, 0, true>;
+    if (!ds->lora_attr_set) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(C::kSmemLora));
+        if (e != cudaSuccess) return fail(TFQ_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+        ds->lora_attr_set = true;
+    }
+    CUtensorMap tmA;
+    tfq_status st = encode_tensor_map_2d(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, A, K, M, K, BK, BM,
+                                         CU_TENSOR_MAP_SWIZZLE_128B);
+    if (st != TFQ_OK) return st;
+    LoraPairMaps maps = {};
+    GemmArgs a;
+    const LinearOperands lin = {W, s_w, bias, N, out};
+    st = pair_linear_setup(&lin, 1, M, K, maps, a);
+    const auto bf16_map = [&](CUtensorMap* m, const void* base, int64_t rows, uint32_t box_rows) {
+        if (st == TFQ_OK)
+            st = encode_tensor_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, l.R, rows, l.R * 2, 64, box_rows,
+                                      CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    bf16_map(&maps.t, t, M + 1, 128);
+    bf16_map(&maps.tg, t, M + 1, 1);
+    bf16_map(&maps.bs, l.Bs, l.n_adapters * N, C::kBHalf);
+    bf16_map(&maps.bsq, l.Bs, l.n_adapters * N, C::kBHalf / 2);
+    if (st != TFQ_OK) return st;
+    maps.idx = l.idx;
+    maps.n_adapters = l.n_adapters;
+    maps.R = l.R;
+    a.s_a = s_a;
+    a.M = static_cast<int>(M);
+    a.K = static_cast<int>(K);
+    a.m_tiles = static_cast<int>((M + BM - 1) / BM);
+    a.k_blocks = static_cast<int>((K + BK - 1) / BK);
+    choose_raster(K, kPBN, a.band_n, a.group_m);
+    a.err = ds->err_word;
+    const int64_t pair_tiles = ((M + 255) / 256) * static_cast<int64_t>(a.n_tiles);
+    if (pair_tiles > INT32_MAX) return fail(TFQ_EUNSUPPORTED, "too many output tiles");
+    const int clusters = static_cast<int>(std::min<int64_t>(pair_tiles, ds->sm_count / 2));
+    a.tail_halves = choose_tail_halves(pair_tiles, clusters);
+    a.round_ctr = take_round_counter(ds);
+    cudaError_t e = launch_kernel(kernel, dim3(2 * clusters), dim3(THREADS), C::kSmemLora, stream, tmA, maps, a);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return e == cudaSuccess ? TFQ_OK : fail(TFQ_ECUDA, "GEMM launch: %s", cudaGetErrorString(e));
+}
 
 tfq_status launch_scaled_fp8_gemm_multi(const void* A, const float* s_a, int64_t M, int64_t K, int n,
                                         const void* const* W, const float* const* s_w, const void* const* bias,

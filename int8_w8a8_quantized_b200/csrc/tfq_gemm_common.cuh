@@ -52,6 +52,12 @@ constexpr uint32_t make_idesc(int m, int n) {
     return fmt | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
+// The same for kind::f16 with BF16 operands (format 1) and an F32 accumulator.
+__host__ __device__ constexpr uint32_t make_idesc_bf16(int m, int n) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
+           (static_cast<uint32_t>(m >> 4) << 24);
+}
+
 // Linears that share their activations (and so the A operand) may run as one
 // CTA-pair launch: at most this many.
 constexpr int kMaxLinears = TFQ_MULTI_MAX_LINEARS;

@@ -19,6 +19,7 @@ enum : uint32_t {
     kErrGemmDrain = 1u << 7,
     kErrSelfTest = 1u << 8,
     kErrQuantStage = 1u << 9,  // a staged-row quantizer gave up waiting for a row load
+    kErrLora = 1u << 10,       // the adapters' first product gave up
 };
 
 struct DeviceState {
@@ -37,6 +38,8 @@ struct DeviceState {
     int next_round_slot = 0;
     // FP8, INT8, FP8/FP16 acc, MXFP8, MXFP8 pair, FP8 pair quantizing its activations
     bool gemm_attr_set[6] = {false, false, false, false, false, false};
+    bool lora_attr_set = false;    // the CTA-pair GEMM with low-rank adapters
+    bool shrink_attr_set = false;  // the adapters' first product
     bool quant_attr_set = false;   // dynamic shared memory limit of the staged-row quantizers
 };
 
@@ -199,6 +202,10 @@ struct LoraCall {
 };
 tfq_status launch_lora_fold(const void* B, const float* scaling, const float* s_w, int64_t n, int64_t N, int64_t R,
                             void* Bs, cudaStream_t stream);
+// (tfq_gemm.cu) the Linear on CTA pairs with t [M + 1, R] bf16, row M zero, beside it
+tfq_status launch_lora_pair_gemm(const void* A, const float* s_a, const void* W, const float* s_w, const void* bias,
+                                 int64_t M, int64_t N, int64_t K, const LoraCall& l, const void* t, void* out,
+                                 cudaStream_t stream, DeviceState* ds);
 size_t lora_workspace_bytes(int64_t M, int64_t R);
 tfq_status launch_scaled_fp8_lora(const void* A_q, const float* s_a, const void* W_q, const float* s_w,
                                   const void* bias, int64_t M, int64_t N, int64_t K, const LoraCall& l, void* out,

@@ -157,3 +157,23 @@ def test_refused_calls():
     with pytest.raises(tfq.TfqError):
         tfq.tfq_scaled_fp8_linear_lora(**{**p, "lora_A": p["lora_A"][:, :12].contiguous(),
                                           "lora_Bs": p["lora_Bs"][..., :12].contiguous()})
+
+
+@pytest.mark.parametrize("M", [20, 200, 600])
+def test_a_broken_adapter_stays_with_its_own_rows(M):
+    """An adapter folded from NaN and inf: rows of other adapters in the same tile keep their values."""
+    p = problem(M, 264, 528, 16, 4, "any", False)
+    clean = tfq.tfq_scaled_fp8_linear_lora(**p)
+    B = torch.randn(4, 264, 16, device="cuda").bfloat16()
+    B[2, ::3], B[2, 1::3] = float("nan"), float("inf")
+    bad = p["lora_Bs"].clone()
+    bad[2] = tfq.tfq_lora_fold(B, None, p["s_w"])[2]
+    assert torch.isfinite(bad).all()
+    y = tfq.tfq_scaled_fp8_linear_lora(**{**p, "lora_Bs": bad})
+    others = p["adapter"] != 2
+    assert torch.equal(y[others], clean[others])
+    x = p["x"].clone()
+    x[7, 3] = float("nan")  # a row's own NaN stays in that row
+    y = tfq.tfq_scaled_fp8_linear_lora(**{**p, "x": x})
+    rows = torch.arange(M, device="cuda") != 7
+    assert torch.equal(y[rows], clean[rows])
