@@ -233,7 +233,7 @@ struct PairCfg {
     static constexpr int kTmemCols = 512;                       // two PBN-column accumulators, power of 2
     static constexpr size_t kRing = static_cast<size_t>(PAIR_STAGES) * (kAStage + kBStage);
     static constexpr size_t kSmem = 1024 + kRing + SMEM_EPI + (2 * PAIR_STAGES + 4 + 1) * 8 + 16;
-    static constexpr size_t kSmemLora = kSmem + 8 + 4 * PAIR_STAGES;  // one barrier, a word per stage
+    static constexpr size_t kSmemLora = kSmem + 8 + 20 * PAIR_STAGES;  // a barrier; two and a word per stage
     static_assert(kSmemLora <= 232448, "shared memory budget exceeded");
     static_assert(2 * PBN <= kTmemCols, "two accumulators must fit in TMEM");
     static_assert(PBN % 64 == 0 && PBN >= 64 && PBN <= 256, "N tile");
@@ -263,9 +263,11 @@ struct PairCfg {
 constexpr int QUANT_WARPS = TFQ_QUANT_WARPS;
 constexpr int QUANT_SEG = 20;  // 16-byte units per lane per segment: a K = 5120 row in one pass
 
-template <int kQuant>
+constexpr int LORA_WARPS = 4;  // row warps of the kernel with low-rank adapters (below)
+
+template <int kQuant, bool kLora = false>
 constexpr int pair_threads() {
-    return THREADS + (kQuant != 0 ? QUANT_WARPS * 32 : 0);
+    return THREADS + (kQuant != 0 ? QUANT_WARPS * 32 : 0) + (kLora ? LORA_WARPS * 32 : 0);
 }
 
 // Rows of the 128-row share of A starting at row0 that must be quantized
@@ -348,22 +350,24 @@ struct LinearOperands {
 // adds sum_r t[m,r] Bs[a,n,r], a = idx[m], to its accumulator, with t and Bs in
 // units of the row's and the column's scale (tfq_lora.cu), so the epilogue's
 // s_a s_w covers both sums.  A tile's accumulator starts with one kind::f16
-// step per adapter present in its 256 rows and 64 columns of the rank, then
-// takes the kind::f8f6f4 steps of the Linear.  For adapter a the A operand is
-// t with the rows of other adapters zero: one tiled load where every row of
-// the CTA's half belongs to a (or none does: a box past the end, all zero
-// fill), else a gather that takes the zero row t[M] for the others, four
-// rows per lane of the producer warp.  The adapters of a tile are enumerated
-// in increasing order from idx by both producers alike; the even one leaves
+// stage per adapter present in its 256 rows and 64 columns of the rank, then
+// takes the kind::f8f6f4 stages of the Linear.  The B operand of such a stage
+// is the adapter's Bs tile (TMA); the A operand is t with the rows of other
+// adapters zero, which four more warps per CTA write: a thread keeps its
+// row's t in registers and stores it to the stage of the row's own adapter,
+// zeros to the others.  (Measured on B200 with 12 adapters of rank 24 in any
+// order, 1777 x 13824 x 5120: a TMA gather of t's rows and a zero row instead
+// took 195 us against 102 us without adapters, 660 us when all CTAs read the
+// same zero row.)  The adapters of a tile are enumerated in increasing order
+// from idx by the producers and the row warps alike; the even producer leaves
 // each stage's kind in shared memory for the MMA thread.  Between the two
 // kinds the MMA thread waits for the first: only instructions of one shape
 // are ordered among themselves.
 struct LoraPairMaps : PairMaps {
-    CUtensorMap t;    // t [M + 1, R] bf16, 64 x 128 boxes
-    CUtensorMap tg;   // the same, one-row boxes for the gather
     CUtensorMap bs;   // Bs [n_adapters * N, R], 64 x PBN / 2 boxes
     CUtensorMap bsq;  // ... 64 x PBN / 4 boxes (half-width tiles)
     const int32_t* idx;
+    const uint4* t;  // [M, R] bf16
     int n_adapters;
     int R;
 };
@@ -378,10 +382,29 @@ __device__ __forceinline__ uint32_t row_adapter(const int32_t* idx, int m, int M
     return a < static_cast<uint32_t>(n_adapters) ? a : 0xFFFFFFFFu;
 }
 
+// The adapters of the 256 rows of tile row tm, eight per lane, for next_adapter.
+struct TileAdapters {
+    uint32_t v[8];
+    uint32_t from;
+    __device__ __forceinline__ TileAdapters(const int32_t* idx, int tm, int M, int n_adapters, int lane) : from(0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = row_adapter(idx, tm * 256 + lane * 8 + i, M, n_adapters);
+    }
+    // The next adapter in increasing order; false past the last.  All lanes call it.
+    __device__ __forceinline__ bool next(uint32_t& a) {
+        a = 0xFFFFFFFFu;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a = min(a, v[i] >= from ? v[i] : 0xFFFFFFFFu);
+        a = __reduce_min_sync(0xFFFFFFFFu, a);
+        from = a + 1;
+        return a != 0xFFFFFFFFu;
+    }
+};
+
 template <int PBN>
 __device__ __forceinline__ void lora_pair_producer(const CUtensorMap& tmA, const LoraPairMaps& maps, const GemmArgs& p,
                                                    uint8_t* sA, uint8_t* sB, uint64_t* full, uint64_t* empty,
-                                                   uint32_t* stage_info, volatile int* abort_flag, int rank,
+                                                   uint64_t* rows_go, uint32_t* stage_info, volatile int* abort_flag, int rank,
                                                    int cluster, int n_clusters, int lane) {
     using C = PairCfg<PBN>;
     const int m_tiles = (p.M + 255) / 256;
@@ -404,58 +427,25 @@ __device__ __forceinline__ void lora_pair_producer(const CUtensorMap& tmA, const
         const int b_row = tn * PBN + (half > 0 ? PBN / 2 : 0) + rank * b_rows;
         const CUtensorMap* tmb = half < 0 ? &maps.b[0] : &maps.bq[0];
         const CUtensorMap* tmbs = half < 0 ? &maps.bs : &maps.bsq;
-        // the adapters of the tile's rows (8 per lane) and of this CTA's half (4 per lane)
-        uint32_t all[8], mine[4];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) all[i] = row_adapter(maps.idx, tm * 256 + lane * 8 + i, p.M, maps.n_adapters);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mine[i] = row_adapter(maps.idx, a_row + lane * 4 + i, p.M, maps.n_adapters);
-        uint32_t flags = kStageFirst;
-        uint32_t from = 0;  // adapters below are done
-        for (;;) {
-            uint32_t a = 0xFFFFFFFFu;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) a = min(a, all[i] >= from ? all[i] : 0xFFFFFFFFu);
-            a = __reduce_min_sync(0xFFFFFFFFu, a);
-            if (a == 0xFFFFFFFFu) break;
-            from = a + 1;
-            bool every = true, any = false;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                any = any || mine[i] == a;
-                every = every && (mine[i] == a || a_row + lane * 4 + i >= p.M);
-            }
-            any = __any_sync(0xFFFFFFFFu, any);
-            every = __all_sync(0xFFFFFFFFu, every);
-            for (int c = 0; c < r_chunks; ++c, ++it) {
+        const uint32_t lora_tx = 2 * static_cast<uint32_t>(b_rows * BK);
+        uint32_t flags = kStageFirst, a;
+        TileAdapters present(maps.idx, tm, p.M, maps.n_adapters, lane);
+        while (ok && present.next(a)) {
+            for (int c = 0; lane == 0 && c < r_chunks; ++c, ++it) {
                 const int st = it % PAIR_STAGES;
-                const uint32_t ph = static_cast<uint32_t>(it / PAIR_STAGES) & 1u;
-                if (lane == 0) ok = mbar_wait(&empty[st], ph ^ 1u, abort_flag);
-                ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
+                ok = mbar_wait(&empty[st], (static_cast<uint32_t>(it / PAIR_STAGES) & 1u) ^ 1u, abort_flag);
                 if (!ok) break;
-                __syncwarp();  // every lane's copies come after the stage was found free
+                mbar_arrive(&rows_go[st]);
                 const uint32_t full_leader = mapa_shared(smem_u32(&full[st]), 0);
-                uint8_t* dst = sA + st * C::kAStage;
-                if (lane == 0) {
-                    if (rank == 0) {
-                        stage_info[st] = flags | kStageLora | static_cast<uint32_t>(min(4, (maps.R - c * 64 + 15) / 16));
-                        mbar_arrive_expect_tx(&full[st], stage_tx);
-                    }
-                    tma_load_2d_pair(sB + st * C::kBStage, tmbs, c * 64, static_cast<int>(a) * p.N + b_row,
-                                     full_leader, pol_b);
-                    // all rows or none: one box, the latter past the last row of t
-                    if (every || !any)
-                        tma_load_2d_pair(dst, &maps.t, c * 64, any ? a_row : p.M + 1, full_leader, pol_a);
+                if (rank == 0) {
+                    stage_info[st] = flags | kStageLora | static_cast<uint32_t>(min(4, (maps.R - c * 64 + 15) / 16));
+                    mbar_arrive_expect_tx(&full[st], lora_tx);
                 }
-                if (any && !every)
-                    tma_gather4_pair(dst + lane * 512, &maps.tg, c * 64, mine[0] == a ? a_row + lane * 4 : p.M,
-                                     mine[1] == a ? a_row + lane * 4 + 1 : p.M,
-                                     mine[2] == a ? a_row + lane * 4 + 2 : p.M,
-                                     mine[3] == a ? a_row + lane * 4 + 3 : p.M, full_leader);
+                tma_load_2d_pair(sB + st * C::kBStage, tmbs, c * 64, static_cast<int>(a) * p.N + b_row, full_leader,
+                                 pol_b);
                 flags = 0;
-                __syncwarp();
             }
-            if (!ok) break;
+            ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
         }
         if (lane == 0) {
             for (int kb = 0; ok && kb < p.k_blocks; ++kb, ++it) {
@@ -475,7 +465,6 @@ __device__ __forceinline__ void lora_pair_producer(const CUtensorMap& tmA, const
             if (ok && rank == 0 && p.round_ctr != nullptr) atomicAdd(p.round_ctr, 1u);
         }
         ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
-        it = __shfl_sync(0xFFFFFFFFu, it, 0);
     }
     if (lane != 0) return;
     if (!ok) give_up(abort_flag, p.err, kErrGemmProducer);
@@ -488,17 +477,73 @@ __device__ __forceinline__ void lora_pair_producer(const CUtensorMap& tmA, const
     }
 }
 
+// The warps that write the A operand of the adapters' stages: thread i of the
+// 128 has row i of this CTA's half.  The CTA's producer tells them through
+// rows_go when such a stage is free (they skip the Linear's stages, so they
+// could not follow the phases of "empty" themselves).
+template <int PBN>
+__device__ __forceinline__ void lora_pair_rows(const LoraPairMaps& maps, const GemmArgs& p, uint8_t* sA,
+                                               uint64_t* rows_go, uint64_t* rows_full,
+                                               volatile int* abort_flag, int rank, int cluster, int n_clusters, int row, int lane) {
+    using C = PairCfg<PBN>;
+    const int m_tiles = (p.M + 255) / 256;
+    const int total_tiles = m_tiles * p.n_tiles;
+    const int r_chunks = (maps.R + 63) / 64;
+    const int units = maps.R / 8;  // 16-byte units of a row of t
+    int it = 0, t, half;
+    uint32_t phase = 0;  // a bit per stage
+    for (int w = cluster; pair_work_item(w, total_tiles, n_clusters, p.tail_halves, t, half); w += n_clusters) {
+        int tm, tn;
+        pair_tile_coords(t, m_tiles, p.n_tiles, p.group_m, p.band_n, tm, tn);
+        const int m = tm * 256 + rank * 128 + row;
+        const uint32_t mine = row_adapter(maps.idx, m, p.M, maps.n_adapters);
+        uint4 v[8];
+        const auto fetch = [&](int c) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                v[u] = mine != 0xFFFFFFFFu && c * 8 + u < units
+                           ? __ldg(maps.t + static_cast<int64_t>(m) * units + c * 8 + u)
+                           : make_uint4(0u, 0u, 0u, 0u);
+        };
+        if (r_chunks == 1) fetch(0);
+        uint32_t a;
+        TileAdapters present(maps.idx, tm, p.M, maps.n_adapters, lane);
+        while (present.next(a)) {
+            for (int c = 0; c < r_chunks; ++c, ++it) {
+                if (r_chunks > 1) fetch(c);
+                const int st = it % PAIR_STAGES;
+                if (!mbar_wait_warp(&rows_go[st], (phase >> st) & 1u, abort_flag)) {
+                    if (lane == 0) give_up(abort_flag, p.err, kErrLora);
+                    return;
+                }
+                phase ^= 1u << st;
+                uint8_t* dst = sA + st * C::kAStage + row * 128;
+                const bool keep = mine == a;
+#pragma unroll
+                for (int u = 0; u < 8; ++u)  // 128-byte swizzle
+                    *reinterpret_cast<uint4*>(dst + ((u ^ (row & 7)) << 4)) = keep ? v[u] : make_uint4(0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&rows_full[st]), 0));
+            }
+        }
+        it += p.k_blocks;
+    }
+}
+
 // The MMA thread of the even CTA: stages as their kind says (see above).
 template <int PBN>
 __device__ __forceinline__ void lora_pair_mma(const GemmArgs& p, uint8_t* sA, uint8_t* sB, uint64_t* full,
                                               uint64_t* empty, uint64_t* tmem_full, uint64_t* tmem_empty,
-                                              uint64_t* order, const volatile uint32_t* stage_info,
+                                              uint64_t* order, uint64_t* rows_full,
+                                              const volatile uint32_t* stage_info,
                                               volatile int* abort_flag, uint32_t tmem_base, int cluster,
                                               int n_clusters) {
     using C = PairCfg<PBN>;
     const int total_tiles = (p.M + 255) / 256 * p.n_tiles;
     int it = 0, tcount = 0, t, half;
     uint32_t order_phase = 0;
+    uint32_t rows_phase = 0;  // a bit per stage
     bool ok = true;
     for (int w = cluster; ok && pair_work_item(w, total_tiles, n_clusters, p.tail_halves, t, half);
          w += n_clusters, ++tcount) {
@@ -517,6 +562,12 @@ __device__ __forceinline__ void lora_pair_mma(const GemmArgs& p, uint8_t* sA, ui
             tc_fence_after();
             const bool was_lora = (info & kStageLora) != 0;
             info = stage_info[st];
+            if ((info & kStageLora) != 0) {
+                ok = mbar_wait_cluster(&rows_full[st], (rows_phase >> st) & 1u, abort_flag);
+                if (!ok) break;
+                rows_phase ^= 1u << st;
+                tc_fence_after();
+            }
             if (was_lora && (info & kStageLora) == 0) {
                 mma_commit_pair(order, 0x1);
                 ok = mbar_wait(order, order_phase, abort_flag);
@@ -546,7 +597,7 @@ __device__ __forceinline__ void lora_pair_mma(const GemmArgs& p, uint8_t* sA, ui
 }
 
 template <int PBN, int kAcc, int kQuant = 0, bool kLora = false>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads<kQuant>(), 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads<kQuant, kLora>(), 1)
     scaled_mm_pair_kernel(const __grid_constant__ CUtensorMap tmA,
                           const __grid_constant__ std::conditional_t<kLora, LoraPairMaps, PairMaps> maps,
                           GemmArgs p) {
@@ -565,7 +616,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads<kQuant>
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     // kLora only (the last 16 bytes hold the two words above)
     uint64_t* order = drain + 3;
-    uint32_t* stage_info = reinterpret_cast<uint32_t*>(order + 1);
+    uint64_t* rows_full = order + 1;
+    uint64_t* rows_go = rows_full + PAIR_STAGES;
+    uint32_t* stage_info = reinterpret_cast<uint32_t*>(rows_go + PAIR_STAGES);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -585,7 +638,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads<kQuant>
             mbar_init(&tmem_empty[i], 2 * EPI_WARPS);
         }
         mbar_init(drain, 1);
-        if constexpr (kLora) mbar_init(order, 1);
+        if constexpr (kLora) {
+            mbar_init(order, 1);
+            for (int i = 0; i < PAIR_STAGES; ++i) {
+                mbar_init(&rows_full[i], 2 * LORA_WARPS);
+                mbar_init(&rows_go[i], 1);
+            }
+        }
         *abort_flag = 0;
         fence_mbar_init();
         prefetch_tensormap(&tmA);
@@ -609,8 +668,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads<kQuant>
     if (warp == 0) {
         // ---------------------------------------------------- TMA producer
         if constexpr (kLora) {
-            lora_pair_producer<PBN>(tmA, maps, p, sA, sB, full, empty, stage_info, abort_flag, static_cast<int>(rank),
-                                    cluster, n_clusters, lane);
+            lora_pair_producer<PBN>(tmA, maps, p, sA, sB, full, empty, rows_go, stage_info, abort_flag,
+                                    static_cast<int>(rank), cluster, n_clusters, lane);
         } else if (lane == 0) {
             uint64_t pol_a, pol_b;
             l2_policies(p, pol_a, pol_b);
@@ -669,7 +728,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads<kQuant>
         // ------------------------------------------- MMA issuer (even CTA)
         if constexpr (kLora) {
             if (lane == 0 && rank == 0) {
-                lora_pair_mma<PBN>(p, sA, sB, full, empty, tmem_full, tmem_empty, order, stage_info, abort_flag,
+                lora_pair_mma<PBN>(p, sA, sB, full, empty, tmem_full, tmem_empty, order, rows_full, stage_info, abort_flag,
                                    tmem_base, cluster, n_clusters);
                 mma_commit_pair(drain, 0x1);
                 if (!mbar_wait(drain, 0, nullptr)) atomicOr(p.err, kErrGemmDrain);
@@ -764,6 +823,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads<kQuant>
         }
         if (lane == 0) bulk_wait<0>();
         __syncwarp();
+    } else if constexpr (kLora) {
+        // ------------------------------------ row warps of the adapters
+        lora_pair_rows<PBN>(maps, p, sA, rows_go, rows_full, abort_flag, static_cast<int>(rank), cluster, n_clusters,
+                            static_cast<int>(threadIdx.x) - THREADS, lane);
     } else {
         // ------------------------------------ quantizer warps (kQuant only)
         if constexpr (kQuant != 0) quantize_rows_for_gemm<kQuant>(p, lane);
@@ -1025,7 +1088,7 @@ tfq_status launch_gemm_multi(const void* A, const float* s_a, int64_t M, int64_t
 
 }  // namespace
 
-// The Linear with the adapters' rows t [M + 1, R] (row M zero) beside it.
+// The Linear with the adapters' first product t [M, R] beside it.
 tfq_status launch_lora_pair_gemm(const void* A, const float* s_a, const void* W, const float* s_w, const void* bias,
                                  int64_t M, int64_t N, int64_t K, const LoraCall& l, const void* t, void* out,
                                  cudaStream_t stream, DeviceState* ds) {
@@ -1051,12 +1114,11 @@ tfq_status launch_lora_pair_gemm(const void* A, const float* s_a, const void* W,
             st = encode_tensor_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, l.R, rows, l.R * 2, 64, box_rows,
                                       CU_TENSOR_MAP_SWIZZLE_128B);
     };
-    bf16_map(&maps.t, t, M + 1, 128);
-    bf16_map(&maps.tg, t, M + 1, 1);
     bf16_map(&maps.bs, l.Bs, l.n_adapters * N, C::kBHalf);
     bf16_map(&maps.bsq, l.Bs, l.n_adapters * N, C::kBHalf / 2);
     if (st != TFQ_OK) return st;
     maps.idx = l.idx;
+    maps.t = static_cast<const uint4*>(t);
     maps.n_adapters = l.n_adapters;
     maps.R = l.R;
     a.s_a = s_a;
@@ -1071,7 +1133,7 @@ tfq_status launch_lora_pair_gemm(const void* A, const float* s_a, const void* W,
     const int clusters = static_cast<int>(std::min<int64_t>(pair_tiles, ds->sm_count / 2));
     a.tail_halves = choose_tail_halves(pair_tiles, clusters);
     a.round_ctr = take_round_counter(ds);
-    cudaError_t e = launch_kernel(kernel, dim3(2 * clusters), dim3(THREADS), C::kSmemLora, stream, tmA, maps, a);
+    cudaError_t e = launch_kernel(kernel, dim3(2 * clusters), dim3(pair_threads<0, true>()), C::kSmemLora, stream, tmA, maps, a);
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? TFQ_OK : fail(TFQ_ECUDA, "GEMM launch: %s", cudaGetErrorString(e));
 }

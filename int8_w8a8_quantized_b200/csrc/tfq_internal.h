@@ -40,6 +40,7 @@ struct DeviceState {
     bool gemm_attr_set[6] = {false, false, false, false, false, false};
     bool lora_attr_set = false;    // the CTA-pair GEMM with low-rank adapters
     bool shrink_attr_set = false;  // the adapters' first product
+    bool small_attr_set = false;   // the Linear with adapters for few rows
     bool quant_attr_set = false;   // dynamic shared memory limit of the staged-row quantizers
 };
 
@@ -202,7 +203,7 @@ struct LoraCall {
 };
 tfq_status launch_lora_fold(const void* B, const float* scaling, const float* s_w, int64_t n, int64_t N, int64_t R,
                             void* Bs, cudaStream_t stream);
-// (tfq_gemm.cu) the Linear on CTA pairs with t [M + 1, R] bf16, row M zero, beside it
+// (tfq_gemm.cu) the Linear on CTA pairs with t [M, R] bf16 beside it
 tfq_status launch_lora_pair_gemm(const void* A, const float* s_a, const void* W, const float* s_w, const void* bias,
                                  int64_t M, int64_t N, int64_t K, const LoraCall& l, const void* t, void* out,
                                  cudaStream_t stream, DeviceState* ds);

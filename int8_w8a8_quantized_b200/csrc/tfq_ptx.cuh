@@ -109,6 +109,28 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, v
     return __all_sync(0xFFFFFFFFu, ok) != 0;
 }
 
+// mbar_wait for arrivals from another CTA of the cluster that publish its
+// shared-memory writes (acquire at cluster scope).
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t i = 0; i < TFQ_WAIT_LIMIT_POLLS; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.b32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        if (ok != 0) return true;
+        if ((i & 31u) == 31u) {
+            if (abort != nullptr && *abort != 0) return false;
+            if (globaltimer_ns() - t0 > TFQ_WAIT_LIMIT_NS) return false;
+        }
+    }
+    return false;
+}
+
 // ------------------------------------------------- programmatic dependent launch
 // A kernel launched with programmatic stream serialization may start while
 // the previous kernel of its stream is still running.  pdl_wait() blocks
@@ -229,18 +251,12 @@ __device__ __forceinline__ void tma_load_2d_pair(void* smem_dst, const CUtensorM
         : "memory");
 }
 
-// Gather of four rows r0..r3 (columns from x) of a 2-D tensor whose map has a
-// one-row box: row i of the result is row ri.  Completion as above.
-__device__ __forceinline__ void tma_gather4_pair(void* smem_dst, const CUtensorMap* map, int32_t x, int32_t r0,
-                                                 int32_t r1, int32_t r2, int32_t r3, uint32_t bar_cluster_addr) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(smem_dst)),
-        "l"(map), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar_cluster_addr)
-        : "memory");
+// Another CTA's shared memory (address from mapa_shared).
+__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+    return v;
 }
-
-// 16 bytes of another CTA's shared memory (address from mapa_shared).
 __device__ __forceinline__ float4 ld_cluster_v4(uint32_t cluster_addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
