@@ -359,10 +359,16 @@ struct LinearOperands {
 // order, 1777 x 13824 x 5120: a TMA gather of t's rows and a zero row instead
 // took 195 us against 102 us without adapters, 660 us when all CTAs read the
 // same zero row.)  The adapters of a tile are enumerated in increasing order
-// from idx by the producers and the row warps alike; the even producer leaves
-// each stage's kind in shared memory for the MMA thread.  Between the two
-// kinds the MMA thread waits for the first: only instructions of one shape
-// are ordered among themselves.
+// from idx by the producers and the row warps alike, from values loaded a tile
+// ahead.
+//
+// Only instructions of one shape and accumulator are ordered among themselves,
+// so the adapters' instructions must be complete before the Linear's first one
+// on the same accumulator.  To wait for that without idling the tensor cores,
+// the adapters' stages of a tile come kLoraLead stages before the end of the
+// tile before it (whose accumulator is the other one): they are long complete
+// when their tile begins.  The even producer leaves each stage's kind in
+// shared memory, and the MMA thread does what it says.
 struct LoraPairMaps : PairMaps {
     CUtensorMap bs;   // Bs [n_adapters * N, R], 64 x PBN / 2 boxes
     CUtensorMap bsq;  // ... 64 x PBN / 4 boxes (half-width tiles)
@@ -371,9 +377,13 @@ struct LoraPairMaps : PairMaps {
     int n_adapters;
     int R;
 };
+constexpr int kLoraLead = 3;
 
 // A stage's contents, for the MMA thread.
-enum : uint32_t { kStageLora = 1u << 3, kStageFirst = 1u << 4, kStageLast = 1u << 5, kStageSteps = 7u };
+enum : uint32_t {
+    kStageSteps = 7u,      // kind::f16 instructions of an adapter's stage
+    kStageLora = 1u << 3,  // an adapter's stage
+};
 
 // idx[m] where it names an adapter, else 0xFFFFFFFF.
 __device__ __forceinline__ uint32_t row_adapter(const int32_t* idx, int m, int M, int n_adapters) {
@@ -382,100 +392,144 @@ __device__ __forceinline__ uint32_t row_adapter(const int32_t* idx, int m, int M
     return a < static_cast<uint32_t>(n_adapters) ? a : 0xFFFFFFFFu;
 }
 
-// The adapters of the 256 rows of tile row tm, eight per lane, for next_adapter.
+// The adapters of the 256 rows of a tile, eight per lane.
 struct TileAdapters {
     uint32_t v[8];
-    uint32_t from;
-    __device__ __forceinline__ TileAdapters(const int32_t* idx, int tm, int M, int n_adapters, int lane) : from(0) {
+    uint32_t from = 0;
+    __device__ __forceinline__ void load(const int32_t* idx, int tm, int M, int n_adapters, int lane) {
+        from = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = row_adapter(idx, tm * 256 + lane * 8 + i, M, n_adapters);
     }
-    // The next adapter in increasing order; false past the last.  All lanes call it.
-    __device__ __forceinline__ bool next(uint32_t& a) {
-        a = 0xFFFFFFFFu;
+    // The next adapter in increasing order, 0xFFFFFFFF past the last.  All lanes call it.
+    __device__ __forceinline__ uint32_t next() {
+        uint32_t a = 0xFFFFFFFFu;
 #pragma unroll
         for (int i = 0; i < 8; ++i) a = min(a, v[i] >= from ? v[i] : 0xFFFFFFFFu);
         a = __reduce_min_sync(0xFFFFFFFFu, a);
         from = a + 1;
-        return a != 0xFFFFFFFFu;
+        return a;
     }
 };
 
+// Work item w of the cluster: its tile coordinates and half; false past the last.
 template <int PBN>
-__device__ __forceinline__ void lora_pair_producer(const CUtensorMap& tmA, const LoraPairMaps& maps, const GemmArgs& p,
-                                                   uint8_t* sA, uint8_t* sB, uint64_t* full, uint64_t* empty,
-                                                   uint64_t* rows_go, uint32_t* stage_info, volatile int* abort_flag, int rank,
-                                                   int cluster, int n_clusters, int lane) {
-    using C = PairCfg<PBN>;
+__device__ __forceinline__ bool lora_work_item(const GemmArgs& p, int w, int n_clusters, int& tm, int& tn, int& half) {
     const int m_tiles = (p.M + 255) / 256;
-    const int total_tiles = m_tiles * p.n_tiles;
-    const int r_chunks = (maps.R + 63) / 64;
+    int t;
+    if (!pair_work_item(w, m_tiles * p.n_tiles, n_clusters, p.tail_halves, t, half)) return false;
+    pair_tile_coords(t, m_tiles, p.n_tiles, p.group_m, p.band_n, tm, tn);
+    return true;
+}
+
+// The producer warp: the whole warp enumerates adapters, lane 0 issues.
+template <int PBN>
+struct LoraProducer {
+    using C = PairCfg<PBN>;
+    const CUtensorMap& tmA;
+    const LoraPairMaps& maps;
+    const GemmArgs& p;
+    uint8_t *sA, *sB;
+    uint64_t *full, *empty, *rows_go;
+    uint32_t* stage_info;
+    volatile int* abort_flag;
+    int rank, lane;
     uint64_t pol_a, pol_b;
-    l2_policies(p, pol_a, pol_b);
     int it = 0;
-    int round = 0, t, half;
     bool ok = true;
-    for (int w = cluster; ok && pair_work_item(w, total_tiles, n_clusters, p.tail_halves, t, half);
-         w += n_clusters, ++round) {
-        if (rank == 0 && lane == 0) pace_round(p.round_ctr, round, total_tiles, n_clusters);
-        __syncwarp();
-        int tm, tn;
-        pair_tile_coords(t, m_tiles, p.n_tiles, p.group_m, p.band_n, tm, tn);
+
+    // Waits for the next stage (lane 0); its index, or -1 after giving up.
+    __device__ __forceinline__ int stage() {
+        const int st = it % PAIR_STAGES;
+        ok = ok && mbar_wait(&empty[st], (static_cast<uint32_t>(it / PAIR_STAGES) & 1u) ^ 1u, abort_flag);
+        return ok ? st : -1;
+    }
+
+    // The adapters' stages of a tile.  All lanes.
+    __device__ __forceinline__ void adapters(TileAdapters& present, int tn, int half) {
+        const int r_chunks = (maps.R + 63) / 64;
         const int b_rows = half < 0 ? C::kBHalf : C::kBHalf / 2;
-        const uint32_t stage_tx = 2 * static_cast<uint32_t>(C::kAStage + b_rows * BK);
-        const int a_row = tm * 256 + rank * 128;
         const int b_row = tn * PBN + (half > 0 ? PBN / 2 : 0) + rank * b_rows;
-        const CUtensorMap* tmb = half < 0 ? &maps.b[0] : &maps.bq[0];
-        const CUtensorMap* tmbs = half < 0 ? &maps.bs : &maps.bsq;
-        const uint32_t lora_tx = 2 * static_cast<uint32_t>(b_rows * BK);
-        uint32_t flags = kStageFirst, a;
-        TileAdapters present(maps.idx, tm, p.M, maps.n_adapters, lane);
-        while (ok && present.next(a)) {
-            for (int c = 0; lane == 0 && c < r_chunks; ++c, ++it) {
-                const int st = it % PAIR_STAGES;
-                ok = mbar_wait(&empty[st], (static_cast<uint32_t>(it / PAIR_STAGES) & 1u) ^ 1u, abort_flag);
-                if (!ok) break;
+        const CUtensorMap* map = half < 0 ? &maps.bs : &maps.bsq;
+        for (uint32_t a = present.next(); a != 0xFFFFFFFFu; a = present.next()) {
+            for (int c = 0; lane == 0 && c < r_chunks; ++c) {
+                const int st = stage();
+                if (st < 0) break;
                 mbar_arrive(&rows_go[st]);
                 const uint32_t full_leader = mapa_shared(smem_u32(&full[st]), 0);
                 if (rank == 0) {
-                    stage_info[st] = flags | kStageLora | static_cast<uint32_t>(min(4, (maps.R - c * 64 + 15) / 16));
-                    mbar_arrive_expect_tx(&full[st], lora_tx);
+                    stage_info[st] = kStageLora | static_cast<uint32_t>(min(4, (maps.R - c * 64 + 15) / 16));
+                    mbar_arrive_expect_tx(&full[st], 2 * static_cast<uint32_t>(b_rows * BK));
                 }
-                tma_load_2d_pair(sB + st * C::kBStage, tmbs, c * 64, static_cast<int>(a) * p.N + b_row, full_leader,
+                tma_load_2d_pair(sB + st * C::kBStage, map, c * 64, static_cast<int>(a) * p.N + b_row, full_leader,
                                  pol_b);
-                flags = 0;
+                ++it;
+            }
+        }
+    }
+
+    // Stages [kb0, kb1) of the Linear (lane 0).
+    __device__ __forceinline__ void linear(int kb0, int kb1, int tm, int tn, int half) {
+        const int b_rows = half < 0 ? C::kBHalf : C::kBHalf / 2;
+        const int b_row = tn * PBN + (half > 0 ? PBN / 2 : 0) + rank * b_rows;
+        const int a_row = tm * 256 + rank * 128;
+        const CUtensorMap* map = half < 0 ? &maps.b[0] : &maps.bq[0];
+        for (int kb = kb0; kb < kb1; ++kb) {
+            const int st = stage();
+            if (st < 0) return;
+            const uint32_t full_leader = mapa_shared(smem_u32(&full[st]), 0);
+            if (rank == 0) {
+                stage_info[st] = 0u;
+                mbar_arrive_expect_tx(&full[st], 2 * static_cast<uint32_t>(C::kAStage + b_rows * BK));
+            }
+            tma_load_2d_pair(sA + st * C::kAStage, &tmA, kb * BK, a_row, full_leader, pol_a);
+            tma_load_2d_pair(sB + st * C::kBStage, map, kb * BK, b_row, full_leader, pol_b);
+            ++it;
+        }
+    }
+
+    __device__ __forceinline__ void run(int cluster, int n_clusters) {
+        const int total_tiles = (p.M + 255) / 256 * p.n_tiles;
+        // at least one stage of the tile (the one that waits for the tile's own
+        // adapters) comes before the next tile's adapters
+        const int lead = min(kLoraLead, p.k_blocks - 1);
+        l2_policies(p, pol_a, pol_b);
+        int tm, tn, half;
+        bool more = lora_work_item<PBN>(p, cluster, n_clusters, tm, tn, half);
+        TileAdapters present;
+        if (more) {
+            present.load(maps.idx, tm, p.M, maps.n_adapters, lane);
+            adapters(present, tn, half);
+        }
+        for (int w = cluster, round = 0; more; w += n_clusters, ++round) {
+            if (rank == 0 && lane == 0) pace_round(p.round_ctr, round, total_tiles, n_clusters);
+            int tm2 = 0, tn2 = 0, half2 = 0;
+            more = lora_work_item<PBN>(p, w + n_clusters, n_clusters, tm2, tn2, half2);
+            if (more) present.load(maps.idx, tm2, p.M, maps.n_adapters, lane);
+            if (lane == 0) linear(0, p.k_blocks - lead, tm, tn, half);
+            __syncwarp();
+            if (more) adapters(present, tn2, half2);
+            if (lane == 0) {
+                linear(p.k_blocks - lead, p.k_blocks, tm, tn, half);
+                if (ok && rank == 0 && p.round_ctr != nullptr) atomicAdd(p.round_ctr, 1u);
             }
             ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
+            if (!ok) break;
+            tm = tm2;
+            tn = tn2;
+            half = half2;
         }
-        if (lane == 0) {
-            for (int kb = 0; ok && kb < p.k_blocks; ++kb, ++it) {
-                const int st = it % PAIR_STAGES;
-                const uint32_t ph = static_cast<uint32_t>(it / PAIR_STAGES) & 1u;
-                ok = mbar_wait(&empty[st], ph ^ 1u, abort_flag);
-                if (!ok) break;
-                const uint32_t full_leader = mapa_shared(smem_u32(&full[st]), 0);
-                if (rank == 0) {
-                    stage_info[st] = flags | static_cast<uint32_t>(BK / UMMA_K) | (kb == p.k_blocks - 1 ? kStageLast : 0u);
-                    mbar_arrive_expect_tx(&full[st], stage_tx);
-                }
-                tma_load_2d_pair(sA + st * C::kAStage, &tmA, kb * BK, a_row, full_leader, pol_a);
-                tma_load_2d_pair(sB + st * C::kBStage, tmb, kb * BK, b_row, full_leader, pol_b);
-                flags = 0;
-            }
-            if (ok && rank == 0 && p.round_ctr != nullptr) atomicAdd(p.round_ctr, 1u);
+        if (lane != 0) return;
+        if (!ok) give_up(abort_flag, p.err, kErrGemmProducer);
+        // As in the plain producer: the even CTA's waits out every load in flight.
+        if (rank == 0) {
+            for (int i = max(0, it - PAIR_STAGES); i < it; ++i)
+                if (!mbar_wait(&full[i % PAIR_STAGES], static_cast<uint32_t>(i / PAIR_STAGES) & 1u, nullptr))
+                    atomicOr(p.err, kErrGemmDrain);
+            pacing_done(p.round_ctr, n_clusters);
         }
-        ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
     }
-    if (lane != 0) return;
-    if (!ok) give_up(abort_flag, p.err, kErrGemmProducer);
-    // As in the plain producer: the even CTA's waits out every load in flight.
-    if (rank == 0) {
-        for (int i = max(0, it - PAIR_STAGES); i < it; ++i)
-            if (!mbar_wait(&full[i % PAIR_STAGES], static_cast<uint32_t>(i / PAIR_STAGES) & 1u, nullptr))
-                atomicOr(p.err, kErrGemmDrain);
-        pacing_done(p.round_ctr, n_clusters);
-    }
-}
+};
 
 // The warps that write the A operand of the adapters' stages: thread i of the
 // 128 has row i of this CTA's half.  The CTA's producer tells them through
@@ -484,19 +538,21 @@ __device__ __forceinline__ void lora_pair_producer(const CUtensorMap& tmA, const
 template <int PBN>
 __device__ __forceinline__ void lora_pair_rows(const LoraPairMaps& maps, const GemmArgs& p, uint8_t* sA,
                                                uint64_t* rows_go, uint64_t* rows_full,
-                                               volatile int* abort_flag, int rank, int cluster, int n_clusters, int row, int lane) {
+                                               volatile int* abort_flag, int rank, int cluster, int n_clusters,
+                                               int row, int lane) {
     using C = PairCfg<PBN>;
-    const int m_tiles = (p.M + 255) / 256;
-    const int total_tiles = m_tiles * p.n_tiles;
     const int r_chunks = (maps.R + 63) / 64;
     const int units = maps.R / 8;  // 16-byte units of a row of t
-    int it = 0, t, half;
+    const int lead = min(kLoraLead, p.k_blocks - 1);  // as the producer
+    int it = 0;
     uint32_t phase = 0;  // a bit per stage
-    for (int w = cluster; pair_work_item(w, total_tiles, n_clusters, p.tail_halves, t, half); w += n_clusters) {
-        int tm, tn;
-        pair_tile_coords(t, m_tiles, p.n_tiles, p.group_m, p.band_n, tm, tn);
+    int tm, tn, half;
+    for (int w = cluster; lora_work_item<PBN>(p, w, n_clusters, tm, tn, half); w += n_clusters) {
+        if (w != cluster) it += p.k_blocks - lead;  // the tile before, up to its last stages
         const int m = tm * 256 + rank * 128 + row;
         const uint32_t mine = row_adapter(maps.idx, m, p.M, maps.n_adapters);
+        TileAdapters present;
+        present.load(maps.idx, tm, p.M, maps.n_adapters, lane);
         uint4 v[8];
         const auto fetch = [&](int c) {
 #pragma unroll
@@ -506,9 +562,7 @@ __device__ __forceinline__ void lora_pair_rows(const LoraPairMaps& maps, const G
                            : make_uint4(0u, 0u, 0u, 0u);
         };
         if (r_chunks == 1) fetch(0);
-        uint32_t a;
-        TileAdapters present(maps.idx, tm, p.M, maps.n_adapters, lane);
-        while (present.next(a)) {
+        for (uint32_t a = present.next(); a != 0xFFFFFFFFu; a = present.next()) {
             for (int c = 0; c < r_chunks; ++c, ++it) {
                 if (r_chunks > 1) fetch(c);
                 const int st = it % PAIR_STAGES;
@@ -527,74 +581,109 @@ __device__ __forceinline__ void lora_pair_rows(const LoraPairMaps& maps, const G
                 if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&rows_full[st]), 0));
             }
         }
-        it += p.k_blocks;
+        if (w != cluster) it += lead;
     }
 }
 
-// The MMA thread of the even CTA: stages as their kind says (see above).
+// The MMA thread of the even CTA.  It follows the producer's order: the first
+// tile's adapters, then for every tile its stages up to the last few, the next
+// tile's adapters, the rest.  How many stages the adapters take it reads from
+// shared memory, stage by stage; everything an instruction of the Linear needs
+// it knows per tile.  (Measured on B200: a loop that took accumulator and shape
+// from each stage's word instead ran 1.4 times as long.)
 template <int PBN>
-__device__ __forceinline__ void lora_pair_mma(const GemmArgs& p, uint8_t* sA, uint8_t* sB, uint64_t* full,
-                                              uint64_t* empty, uint64_t* tmem_full, uint64_t* tmem_empty,
-                                              uint64_t* order, uint64_t* rows_full,
-                                              const volatile uint32_t* stage_info,
-                                              volatile int* abort_flag, uint32_t tmem_base, int cluster,
-                                              int n_clusters) {
+struct LoraMma {
     using C = PairCfg<PBN>;
-    const int total_tiles = (p.M + 255) / 256 * p.n_tiles;
-    int it = 0, tcount = 0, t, half;
-    uint32_t order_phase = 0;
+    const GemmArgs& p;
+    uint8_t *sA, *sB;
+    uint64_t *full, *empty, *order, *rows_full;
+    const volatile uint32_t* stage_info;
+    volatile int* abort_flag;
+    int it = 0;
     uint32_t rows_phase = 0;  // a bit per stage
     bool ok = true;
-    for (int w = cluster; ok && pair_work_item(w, total_tiles, n_clusters, p.tail_halves, t, half);
-         w += n_clusters, ++tcount) {
-        const int buf = tcount & 1;
-        const uint32_t use = static_cast<uint32_t>(tcount >> 1);
-        ok = mbar_wait(&tmem_empty[buf], (use & 1u) ^ 1u, abort_flag);
-        if (!ok) break;
-        tc_fence_after();
-        const int n = half < 0 ? PBN : PBN / 2;
-        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * PBN);
-        uint32_t info = 0;
-        do {
+
+    __device__ __forceinline__ bool wait_full() {
+        ok = ok && mbar_wait(&full[it % PAIR_STAGES], static_cast<uint32_t>(it / PAIR_STAGES) & 1u, abort_flag);
+        return ok;
+    }
+
+    // The adapters' stages, if the next stage is one; true if there were any.
+    __device__ __forceinline__ bool adapters(uint64_t* tmem_empty_bar, uint32_t empty_parity, uint32_t d_tmem, int n) {
+        const uint32_t idesc = make_idesc_bf16(256, n);
+        uint32_t acc = 0;
+        while (wait_full()) {
             const int st = it % PAIR_STAGES;
-            ok = mbar_wait(&full[st], static_cast<uint32_t>(it / PAIR_STAGES) & 1u, abort_flag);
+            const uint32_t info = stage_info[st];
+            if ((info & kStageLora) == 0) break;
+            ok = acc != 0 || mbar_wait(tmem_empty_bar, empty_parity, abort_flag);
+            ok = ok && mbar_wait_cluster(&rows_full[st], (rows_phase >> st) & 1u, abort_flag);
             if (!ok) break;
+            rows_phase ^= 1u << st;
             tc_fence_after();
-            const bool was_lora = (info & kStageLora) != 0;
-            info = stage_info[st];
-            if ((info & kStageLora) != 0) {
-                ok = mbar_wait_cluster(&rows_full[st], (rows_phase >> st) & 1u, abort_flag);
-                if (!ok) break;
-                rows_phase ^= 1u << st;
-                tc_fence_after();
-            }
-            if (was_lora && (info & kStageLora) == 0) {
-                mma_commit_pair(order, 0x1);
-                ok = mbar_wait(order, order_phase, abort_flag);
-                if (!ok) break;
-                order_phase ^= 1u;
-                tc_fence_after();
-            }
             const uint64_t a_desc = sw128_kmajor_desc(sA + st * C::kAStage);
             const uint64_t b_desc = sw128_kmajor_desc(sB + st * C::kBStage);
-            uint32_t acc = (info & kStageFirst) != 0 ? 0u : 1u;
-            if ((info & kStageLora) != 0) {
-                const uint32_t idesc = make_idesc_bf16(256, n);
-                for (uint32_t k = 0; k < (info & kStageSteps); ++k, acc = 1u)
-                    mma_bf16_pair(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc, acc);
-            } else {
-                const uint32_t idesc = make_idesc<kAccF32>(256, n);
 #pragma unroll
-                for (int k = 0; k < BK / UMMA_K; ++k, acc = 1u)
-                    mma_e4m3_pair<false>(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc, acc);
+            for (uint32_t k = 0; k < 4; ++k) {
+                if (k < (info & kStageSteps)) mma_bf16_pair(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc, acc);
+                acc = 1;
             }
             mma_commit_pair(&empty[st], 0x3);
             ++it;
-        } while ((info & kStageLast) == 0);
-        if (ok) mma_commit_pair(&tmem_full[buf], 0x3);
+        }
+        if (acc != 0) mma_commit_pair(order, 0x1);
+        return acc != 0;
     }
-    if (!ok) give_up(abort_flag, p.err, kErrGemmMma);
-}
+
+    // Stages [kb0, kb1) of the Linear; acc0: the accumulator already holds something.
+    __device__ __forceinline__ void linear(int kb0, int kb1, uint32_t d_tmem, uint32_t idesc, bool acc0) {
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+            if (!wait_full()) return;
+            const int st = it % PAIR_STAGES;
+            tc_fence_after();
+            const uint64_t a_desc = sw128_kmajor_desc(sA + st * C::kAStage);
+            const uint64_t b_desc = sw128_kmajor_desc(sB + st * C::kBStage);
+#pragma unroll
+            for (int k = 0; k < BK / UMMA_K; ++k)
+                mma_e4m3_pair<false>(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc, (kb > 0 || k > 0 || acc0) ? 1u : 0u);
+            mma_commit_pair(&empty[st], 0x3);
+        }
+    }
+
+    __device__ __forceinline__ void run(uint64_t* tmem_full, uint64_t* tmem_empty, uint32_t tmem_base, int cluster,
+                                        int n_clusters) {
+        const int total_tiles = (p.M + 255) / 256 * p.n_tiles;
+        const int lead = min(kLoraLead, p.k_blocks - 1);  // as the producer
+        uint32_t order_phase = 0;
+        int t, half;
+        bool more = pair_work_item(cluster, total_tiles, n_clusters, p.tail_halves, t, half);
+        // tile number c uses accumulator c & 1, for the (c >> 1)-th time
+        bool after_lora = more && adapters(&tmem_empty[0], 1u, tmem_base, half < 0 ? PBN : PBN / 2);
+        for (int w = cluster, c = 0; more && ok; w += n_clusters, ++c) {
+            const int buf = c & 1;
+            const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * PBN);
+            const uint32_t idesc = make_idesc<kAccF32>(256, half < 0 ? PBN : PBN / 2);
+            if (after_lora) {
+                ok = mbar_wait(order, order_phase, abort_flag);
+                order_phase ^= 1u;
+            } else {
+                ok = mbar_wait(&tmem_empty[buf], (static_cast<uint32_t>(c >> 1) & 1u) ^ 1u, abort_flag);
+            }
+            if (!ok) break;
+            tc_fence_after();
+            linear(0, p.k_blocks - lead, d_tmem, idesc, after_lora);
+            int half2 = -1;
+            more = pair_work_item(w + n_clusters, total_tiles, n_clusters, p.tail_halves, t, half2);
+            const bool after2 =
+                more && adapters(&tmem_empty[buf ^ 1], (static_cast<uint32_t>((c + 1) >> 1) & 1u) ^ 1u,
+                                 tmem_base + static_cast<uint32_t>((buf ^ 1) * PBN), half2 < 0 ? PBN : PBN / 2);
+            linear(p.k_blocks - lead, p.k_blocks, d_tmem, idesc, after_lora);
+            if (ok) mma_commit_pair(&tmem_full[buf], 0x3);
+            half = half2;
+            after_lora = after2;
+        }
+    }
+};
 
 template <int PBN, int kAcc, int kQuant = 0, bool kLora = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads<kQuant, kLora>(), 1)
@@ -668,8 +757,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads<kQuant,
     if (warp == 0) {
         // ---------------------------------------------------- TMA producer
         if constexpr (kLora) {
-            lora_pair_producer<PBN>(tmA, maps, p, sA, sB, full, empty, rows_go, stage_info, abort_flag,
-                                    static_cast<int>(rank), cluster, n_clusters, lane);
+            LoraProducer<PBN> producer = {tmA,        maps,       p,
+                                          sA,         sB,         full,
+                                          empty,      rows_go,    stage_info,
+                                          abort_flag, static_cast<int>(rank), lane};
+            producer.run(cluster, n_clusters);
         } else if (lane == 0) {
             uint64_t pol_a, pol_b;
             l2_policies(p, pol_a, pol_b);
@@ -728,8 +820,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads<kQuant,
         // ------------------------------------------- MMA issuer (even CTA)
         if constexpr (kLora) {
             if (lane == 0 && rank == 0) {
-                lora_pair_mma<PBN>(p, sA, sB, full, empty, tmem_full, tmem_empty, order, rows_full, stage_info, abort_flag,
-                                   tmem_base, cluster, n_clusters);
+                LoraMma<PBN> mma = {p, sA, sB, full, empty, order, rows_full, stage_info, abort_flag};
+                mma.run(tmem_full, tmem_empty, tmem_base, cluster, n_clusters);
+                if (!mma.ok) give_up(abort_flag, p.err, kErrGemmMma);
                 mma_commit_pair(drain, 0x1);
                 if (!mbar_wait(drain, 0, nullptr)) atomicOr(p.err, kErrGemmDrain);
             }
