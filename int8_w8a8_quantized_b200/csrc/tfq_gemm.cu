@@ -578,7 +578,7 @@ __device__ __forceinline__ void lora_pair_rows(const LoraPairMaps& maps, const G
                     *reinterpret_cast<uint4*>(dst + ((u ^ (row & 7)) << 4)) = keep ? v[u] : make_uint4(0u, 0u, 0u, 0u);
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&rows_full[st]), 0));
+                if (lane == 0) mbar_arrive_cluster_local_data(mapa_shared(smem_u32(&rows_full[st]), 0));
             }
         }
         if (w != cluster) it += lead;

@@ -236,6 +236,13 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t local_addr, uint32_t ra
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
+// The same without a cluster-scope release: for a warp that has written its own
+// CTA's shared memory for the tensor cores of its own SM and fenced it towards
+// the async proxy (fence_proxy_async_smem).  The release form also waits for
+// everything else the thread has outstanding, which measured 1000 cycles.
+__device__ __forceinline__ void mbar_arrive_cluster_local_data(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
