@@ -443,9 +443,10 @@ TFQ_API tfq_status tfq_rope_axes(const void *q, int64_t q_row_stride, int64_t q_
  * Errors: those of tfq_scaled_fp8_linear; TFQ_EINVAL (n_adapters or R negative,
  * R % 8 != 0, a null pointer, x, lora_A, lora_Bs or workspace not 16-byte
  * aligned, adapter not 4-byte aligned), TFQ_EUNSUPPORTED (R > TFQ_LORA_MAX_RANK,
- * n_adapters * max(N, R) >= 2^31).
+ * n_adapters > TFQ_LORA_MAX_ADAPTERS, n_adapters * max(N, R) >= 2^31 - 1024).
  */
 #define TFQ_LORA_MAX_RANK 256
+#define TFQ_LORA_MAX_ADAPTERS (1 << 22)
 TFQ_API size_t tfq_scaled_fp8_linear_lora_workspace_bytes(int64_t M, int64_t R);
 TFQ_API tfq_status tfq_scaled_fp8_linear_lora(const void *A_q, const float *s_a, const void *W_q, const float *s_w,
                                               const void *bias_bf16, int64_t M, int64_t N, int64_t K,

@@ -199,6 +199,8 @@ tfq_status tfq_scaled_fp8_linear_lora(const void* A_q, const float* s_a, const v
     if (n_adapters < 0 || R < 0) return fail(TFQ_EINVAL, "negative size");
     if (R % 8 != 0) return fail(TFQ_EINVAL, "R=%lld is not a multiple of 8", (long long)R);
     if (R > TFQ_LORA_MAX_RANK) return fail(TFQ_EUNSUPPORTED, "R=%lld above %d", (long long)R, TFQ_LORA_MAX_RANK);
+    if (n_adapters > TFQ_LORA_MAX_ADAPTERS)
+        return fail(TFQ_EUNSUPPORTED, "n_adapters=%lld above %d", (long long)n_adapters, TFQ_LORA_MAX_ADAPTERS);
     if (n_adapters > 0 && n_adapters > (kLimit - 1024) / std::max<int64_t>(1, std::max(N, R)))
         return fail(TFQ_EUNSUPPORTED, "size too large");
     if (M == 0 || N == 0) return TFQ_OK;

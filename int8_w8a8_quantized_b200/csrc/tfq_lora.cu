@@ -40,26 +40,36 @@ __global__ void __launch_bounds__(256) lora_fold_kernel(const __nv_bfloat16* B, 
 }
 
 // ---------------------------------------------------------------------------
-// First product, rows in tiles of 128 (lora_shrink_kernel):
+// First product, many rows (lora_shrink_kernel):
 //   t[m, r] = bf16(sum_k x[m,k] A[idx[m],r,k] / s_a[m]).
-// A CTA takes 128 rows and streams their x through shared memory once for as
-// many adapters as fit 128 accumulator columns (each Rn = R rounded up to 16
-// columns wide), so a tile whose rows belong to one adapter, or to a few of
-// low rank, reads x once; more adapters take further passes over x (from L2)
-// or, while the grid is small, other CTAs.  Bound by HBM: x is M K bf16
-// values against 2 R flops each, far below the tensor cores' ratio; the
-// tensor cores are used because plain FMAs would not keep up from R = 16 on.
-// Few tiles split K over a cluster of S CTAs, whose partial sums meet in
+// Rows are taken in blocks of kShrinkRows.  A CTA puts its block's rows in the
+// order of their adapters and cuts that into items of up to 128 rows of one
+// adapter, which the block's `item_ctas` CTAs share out.  An item is a
+// [128, K] x [K, Rn] product on the tensor cores (Rn = R rounded up to 16):
+// its x rows come as one TMA box where they are consecutive, else row by row
+// through the registers of the epilogue's warps, which are idle then; either
+// way every row of x is read once, and A once per item (from L2).  (Measured
+// on B200, 12 adapters of rank 64 in any order, 9472 x 5120: streaming a
+// tile's x once for two adapters at a time and keeping each row's own product
+// 242 us, TMA gathers of four rows 116 us (some 56 cycles each), cp.async
+// 163 us (the fence behind each step waits for all copies in flight).)  Bound
+// by HBM: 2 R flops per value of x are far below the tensor cores' ratio; they
+// are used because plain FMAs would not keep up.
+// Few rows split K over a cluster of S CTAs, whose partial sums meet in
 // shared memory and are added in rank order (the same bits every time).
 // Roles as in the GEMM: warp 0 TMA producer, warp 1 MMA, warps 2..5 epilogue.
 constexpr int kShrinkThreads = 192;
 constexpr int kShrinkMaxStages = 8;
 constexpr int kShrinkXStage = 128 * 128;  // 128 rows x 64 bf16
+constexpr int kShrinkRows = 512;
+constexpr int kShrinkTable = 1024;  // up to so many adapters the rows are counted, more are ranked by comparison
+constexpr uint32_t kNoAdapter = 0xFFFFFFFFu / kShrinkRows;  // a key's adapter where the row has none
 
 struct ShrinkArgs {
     int M, R, Rn, n_adapters;
-    int per_pass;  // adapters per pass
-    int stages, k_blocks, splits, pass_ctas;
+    int stages, k_blocks, splits, item_ctas;
+    int K;
+    const __nv_bfloat16* x;
     const int32_t* idx;
     const float* s_a;
     __nv_bfloat16* t;
@@ -69,44 +79,230 @@ struct ShrinkArgs {
 // Shared memory behind the stages and, with splits > 1, the partial sums.
 struct ShrinkTail {
     uint64_t full[kShrinkMaxStages], empty[kShrinkMaxStages];
+    uint64_t x_full[kShrinkMaxStages];  // x rows that came through registers
     uint64_t tmem_full, tmem_empty, drain;
     uint32_t tmem_slot;
     int abort_flag;
-    int count;
-    uint32_t list[128];  // the tile's adapters, increasing
-    int16_t place[128];  // a row's adapter in that list, -1: none
+    int segments;
+    alignas(16) uint32_t key[kShrinkRows];  // adapter * kShrinkRows + row in the block
+    uint32_t order[kShrinkRows];            // the keys of rows with an adapter, in increasing order
+    int16_t segment[kShrinkRows + 1];       // where each adapter's rows begin in that order, and the end
+    int16_t count[kShrinkTable];            // rows per adapter, then where they begin
 };
 
-__host__ __device__ constexpr int shrink_stage_bytes(int cols) { return kShrinkXStage + cols * 128; }
+__host__ __device__ constexpr int shrink_stage_bytes(int rn) { return kShrinkXStage + rn * 128; }
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-__global__ void __launch_bounds__(kShrinkThreads)
+// The items of a block that are this CTA's: next() is false past the last.
+struct ShrinkItems {
+    const ShrinkTail& s;
+    int first, step;       // this CTA's items: first, first + step, ...
+    int segment = 0, at = 0, item = 0;
+    int start = 0, len = 0;  // of the present item, in the order
+
+    __device__ __forceinline__ bool next() {
+        for (; segment < s.segments; ++segment, at = 0) {
+            const int begin = s.segment[segment], end = s.segment[segment + 1];
+            for (; begin + at < end; ++item) {
+                start = begin + at;
+                len = min(128, end - start);
+                at += 128;
+                if (item % step == first) {
+                    ++item;
+                    return true;
+                }
+            }
+        }
+        return false;
+    }
+    __device__ __forceinline__ uint32_t adapter() const { return s.order[start] / kShrinkRows; }
+    __device__ __forceinline__ int row(int i) const { return static_cast<int>(s.order[start + i] % kShrinkRows); }
+    __device__ __forceinline__ bool box() const { return row(len - 1) - row(0) == len - 1; }  // consecutive rows
+};
+
+// Fills order, segment and segments from key (all threads; count zeroed).
+// in_order: the keys of rows with an adapter increase already (requests one
+// after the other, the usual case).
+__device__ __forceinline__ void order_rows(ShrinkTail& s, int n_adapters, bool in_order) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t before = (1u << lane) - 1u;
+    if (in_order) {
+        if (warp != 0) return;
+        int begin = 0, n = 0;
+        uint32_t last = kNoAdapter;  // the adapter of the row before
+#pragma unroll
+        for (int c = 0; c < kShrinkRows / 32; ++c) {
+            const uint32_t key = s.key[c * 32 + lane], a = key / kShrinkRows;
+            uint32_t prev = __shfl_up_sync(0xFFFFFFFFu, a, 1);
+            if (lane == 0) prev = last;
+            const uint32_t has = __ballot_sync(0xFFFFFFFFu, a != kNoAdapter);
+            const uint32_t begins = __ballot_sync(0xFFFFFFFFu, a != kNoAdapter && a != prev);
+            const int at = begin + __popc(has & before);
+            if (a != kNoAdapter) s.order[at] = key;
+            if ((begins >> lane & 1u) != 0) s.segment[n + __popc(begins & before)] = static_cast<int16_t>(at);
+            begin += __popc(has);
+            n += __popc(begins);
+            last = __shfl_sync(0xFFFFFFFFu, a, 31);
+        }
+        if (lane == 0) {
+            s.segment[n] = static_cast<int16_t>(begin);
+            s.segments = n;
+        }
+        return;
+    }
+    if (n_adapters <= kShrinkTable) {
+        if (warp != 0) return;
+        uint32_t key[kShrinkRows / 32];
+        int place[kShrinkRows / 32];  // among the rows of its adapter
+#pragma unroll
+        for (int c = 0; c < kShrinkRows / 32; ++c) {
+            key[c] = s.key[c * 32 + lane];
+            const uint32_t a = key[c] / kShrinkRows;
+            const uint32_t same = __match_any_sync(0xFFFFFFFFu, a);
+            const int done = a != kNoAdapter ? s.count[a] : 0;
+            place[c] = done + __popc(same & before);
+            __syncwarp();
+            if (a != kNoAdapter && (same & before) == 0) s.count[a] = static_cast<int16_t>(done + __popc(same));
+            __syncwarp();
+        }
+        int begin = 0, n = 0;  // rows and segments so far
+        for (int e0 = 0; e0 < n_adapters; e0 += 32) {
+            const int mine = s.count[e0 + lane];
+            int sum = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+                if (lane >= o) sum += v;
+            }
+            const uint32_t used = __ballot_sync(0xFFFFFFFFu, mine > 0);
+            s.count[e0 + lane] = static_cast<int16_t>(begin + sum - mine);
+            if (mine > 0) s.segment[n + __popc(used & before)] = static_cast<int16_t>(begin + sum - mine);
+            n += __popc(used);
+            begin += __shfl_sync(0xFFFFFFFFu, sum, 31);
+        }
+        if (lane == 0) {
+            s.segment[n] = static_cast<int16_t>(begin);
+            s.segments = n;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < kShrinkRows / 32; ++c) {
+            const uint32_t a = key[c] / kShrinkRows;
+            if (a != kNoAdapter) s.order[s.count[a] + place[c]] = key[c];
+        }
+        return;
+    }
+    for (int i = threadIdx.x; i < kShrinkRows; i += kShrinkThreads) {
+        const uint32_t key = s.key[i];
+        int rank = 0;
+#pragma unroll 4
+        for (int j = 0; j < kShrinkRows / 4; ++j) {
+            const uint4 k = reinterpret_cast<const uint4*>(s.key)[j];
+            rank += (k.x < key) + (k.y < key) + (k.z < key) + (k.w < key);
+        }
+        s.order[rank] = key;
+    }
+    __syncthreads();
+    if (warp != 0) return;
+    int n = 0;
+    for (int i0 = 0; i0 < kShrinkRows; i0 += 32) {
+        const int i = i0 + lane;
+        const uint32_t a = s.order[i] / kShrinkRows;
+        const bool begins = i == 0 || s.order[i - 1] / kShrinkRows != a;
+        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, begins);
+        if (begins) s.segment[n + __popc(mask & before)] = static_cast<int16_t>(i);
+        n += __popc(mask);
+    }
+    if (lane == 0) {
+        s.segment[n] = kShrinkRows;
+        // the last segment may be the rows without an adapter
+        s.segments = s.order[kShrinkRows - 1] / kShrinkRows == kNoAdapter ? n - 1 : n;
+    }
+}
+
+// The x rows of an item of up to 16 * NP rows, by the epilogue's 128 threads:
+// eight threads a row, 16 rows at a time, 8 / NP steps of K at once, and the
+// next such batch in flight while the present one is stored: 16 loads a thread
+// whatever the item's rows.  False after giving up.
+template <int NP>
+__device__ __forceinline__ bool x_rows(ShrinkTail& s, const ShrinkArgs& p, uint8_t* smem, const ShrinkItems& item,
+                                       int row0, int kb0, int kb1, int& it) {
+    constexpr int kSteps = 8 / NP;
+    const int lane = threadIdx.x & 31, chunk = threadIdx.x & 7, sub = (threadIdx.x - 64) >> 3;
+    const int stage_bytes = shrink_stage_bytes(p.Rn);
+    const __nv_bfloat16* src[NP];
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+        const int r = sub + 16 * j;
+        src[j] = r < item.len ? p.x + static_cast<int64_t>(row0 + item.row(r)) * p.K + chunk * 8 : nullptr;
+    }
+    const auto load = [&](uint4(&v)[8], int kb) {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const bool in = kb + i < kb1 && (kb + i) * 64 + chunk * 8 < p.K;
+#pragma unroll
+            for (int j = 0; j < NP; ++j)
+                v[i * NP + j] = in && src[j] != nullptr ? ldg_nc_v4(reinterpret_cast<const uint4*>(src[j] + (kb + i) * 64))
+                                                        : make_uint4(0u, 0u, 0u, 0u);
+        }
+    };
+    const auto store = [&](const uint4(&v)[8], int kb) {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            if (kb + i >= kb1) break;
+            const int st = it % p.stages;
+            if (!mbar_wait_warp(&s.empty[st], (static_cast<uint32_t>(it / p.stages) & 1u) ^ 1u, &s.abort_flag)) return false;
+            uint8_t* sx = smem + st * stage_bytes;
+#pragma unroll
+            for (int j = 0; j < NP; ++j) {  // 128-byte swizzle
+                const int r = sub + 16 * j;
+                if (src[j] != nullptr) *reinterpret_cast<uint4*>(sx + r * 128 + ((chunk ^ (r & 7)) << 4)) = v[i * NP + j];
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.x_full[st]);
+            ++it;
+        }
+        return true;
+    };
+    uint4 v0[8], v1[8];
+    load(v0, kb0);
+    for (int kb = kb0; kb < kb1; kb += 2 * kSteps) {
+        load(v1, kb + kSteps);
+        if (!store(v0, kb)) return false;
+        load(v0, kb + 2 * kSteps);
+        if (!store(v1, kb + kSteps)) return false;
+    }
+    return true;
+}
+
+__global__ void __launch_bounds__(kShrinkThreads, 2)
     lora_shrink_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmA,
                        const ShrinkArgs p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int cols = p.per_pass * p.Rn;
-    const int stage_bytes = shrink_stage_bytes(cols);
+    const int stage_bytes = shrink_stage_bytes(p.Rn);
     float* part = reinterpret_cast<float*>(smem + p.stages * stage_bytes);  // [128][R], splits > 1
     ShrinkTail* s = reinterpret_cast<ShrinkTail*>(reinterpret_cast<uint8_t*>(part) +
                                                   (p.splits > 1 ? 128 * p.R * sizeof(float) : 0));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = p.splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-    const int item = blockIdx.x / p.splits;
-    const int tile = item / p.pass_ctas;
-    const int first_pass = item - tile * p.pass_ctas;
-    const int row0 = tile * 128;
+    const int unit = blockIdx.x / p.splits;
+    const int block = unit / p.item_ctas;
+    const int row0 = block * kShrinkRows;
+    const int rows = min(kShrinkRows, p.M - row0);
     uint32_t tmem_cols = 32;
-    while (static_cast<int>(tmem_cols) < cols) tmem_cols *= 2;
+    while (static_cast<int>(tmem_cols) < p.Rn) tmem_cols *= 2;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.stages; ++i) {
             mbar_init(&s->full[i], 1);
             mbar_init(&s->empty[i], 1);
+            mbar_init(&s->x_full[i], 4);
         }
         mbar_init(&s->tmem_full, 1);
         mbar_init(&s->tmem_empty, 4);
@@ -122,32 +318,18 @@ __global__ void __launch_bounds__(kShrinkThreads)
     }
     pdl_allow_next();
     pdl_wait();
-    if (warp == 0) {  // the tile's adapters in increasing order, and each row's place among them
-        uint32_t v[4];
-        int place[4] = {-1, -1, -1, -1};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int m = row0 + lane * 4 + i;
-            const uint32_t a = m < p.M ? static_cast<uint32_t>(__ldg(p.idx + m)) : 0xFFFFFFFFu;
-            v[i] = a < static_cast<uint32_t>(p.n_adapters) ? a : 0xFFFFFFFFu;
-        }
-        int n = 0;
-        for (uint32_t from = 0;; ++n) {
-            uint32_t a = 0xFFFFFFFFu;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) a = min(a, v[i] >= from ? v[i] : 0xFFFFFFFFu);
-            a = __reduce_min_sync(0xFFFFFFFFu, a);
-            if (a == 0xFFFFFFFFu) break;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (v[i] == a) place[i] = n;
-            if (lane == 0) s->list[n] = a;
-            from = a + 1;
-        }
-        if (lane == 0) s->count = n;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s->place[lane * 4 + i] = static_cast<int16_t>(place[i]);
+    // Keys; rows past the end and rows without an adapter sort behind all others.
+    for (int i = threadIdx.x; i < kShrinkRows; i += kShrinkThreads) {
+        const uint32_t a = i < rows ? static_cast<uint32_t>(__ldg(p.idx + row0 + i)) : 0xFFFFFFFFu;
+        s->key[i] = (a < static_cast<uint32_t>(p.n_adapters) ? a : kNoAdapter) * kShrinkRows + i;
     }
+    for (int i = threadIdx.x; i < kShrinkTable; i += kShrinkThreads) s->count[i] = 0;
+    __syncthreads();
+    bool in_order = true;  // a row without an adapter may stand anywhere between two runs
+    for (int i = threadIdx.x; i < kShrinkRows - 1; i += kShrinkThreads)
+        in_order = in_order && (s->key[i] < s->key[i + 1] || s->key[i] / kShrinkRows == kNoAdapter);
+    in_order = __syncthreads_and(in_order);
+    order_rows(*s, p.n_adapters, in_order);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -155,38 +337,46 @@ __global__ void __launch_bounds__(kShrinkThreads)
     volatile int* abort_flag = &s->abort_flag;
     const int kb0 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * rank / p.splits);
     const int kb1 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * (rank + 1) / p.splits);
-    const int count = s->count;
+
     int it = 0;
     bool ok = true;
-    uint32_t turn = 0;  // passes done by this CTA
-    for (int base = first_pass * p.per_pass; base < count; base += p.pass_ctas * p.per_pass, ++turn) {
-        const int n = min(p.per_pass, count - base);
+    uint32_t turn = 0;  // items done by this CTA
+    uint32_t x_phase = 0;  // a bit per stage
+    ShrinkItems item = {*s, unit - block * p.item_ctas, p.item_ctas};
+    for (; item.next(); ++turn) {
         if (warp == 0) {
             if (lane == 0) {
+                const int a_row = static_cast<int>(item.adapter()) * p.R;
+                const int first = row0 + item.row(0);
+                const bool box = item.box();
+                const uint32_t tx = static_cast<uint32_t>((box ? kShrinkXStage : 0) + p.Rn * 128);
                 for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
                     const int st = it % p.stages;
                     ok = mbar_wait(&s->empty[st], (static_cast<uint32_t>(it / p.stages) & 1u) ^ 1u, abort_flag);
-                    if (!ok) {
-                        *abort_flag = 1;
-                        atomicOr(p.err, kErrLora);
-                        break;
-                    }
+                    if (!ok) break;
                     uint8_t* sx = smem + st * stage_bytes;
-                    mbar_arrive_expect_tx(&s->full[st], kShrinkXStage + n * p.Rn * 128);
-                    tma_load_2d(sx, &tmX, kb * 64, row0, &s->full[st]);
-                    for (int i = 0; i < n; ++i)
-                        tma_load_2d(sx + kShrinkXStage + i * p.Rn * 128, &tmA, kb * 64,
-                                    static_cast<int>(s->list[base + i]) * p.R, &s->full[st]);
+                    mbar_arrive_expect_tx(&s->full[st], tx);
+                    if (box) tma_load_2d(sx, &tmX, kb * 64, first, &s->full[st]);
+                    tma_load_2d(sx + kShrinkXStage, &tmA, kb * 64, a_row, &s->full[st]);
                 }
+            }
+            if (!ok && lane == 0) {
+                *abort_flag = 1;
+                atomicOr(p.err, kErrLora);
             }
         } else if (warp == 1) {
             if (lane == 0) {
                 if (ok) ok = mbar_wait(&s->tmem_empty, (turn & 1u) ^ 1u, abort_flag);
                 tc_fence_after();
-                const uint32_t idesc = make_idesc_bf16(128, n * p.Rn);
+                const uint32_t idesc = make_idesc_bf16(128, p.Rn);
+                const bool box = item.box();
                 for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
                     const int st = it % p.stages;
                     ok = mbar_wait(&s->full[st], static_cast<uint32_t>(it / p.stages) & 1u, abort_flag);
+                    if (ok && !box) {
+                        ok = mbar_wait(&s->x_full[st], (x_phase >> st) & 1u, abort_flag);
+                        x_phase ^= 1u << st;
+                    }
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t a_desc = sw128_kmajor_desc(smem + st * stage_bytes);
@@ -205,43 +395,45 @@ __global__ void __launch_bounds__(kShrinkThreads)
             }
         } else {
             const int quarter = warp & 3;
-            const int row = quarter * 32 + lane;
-            const int m = row0 + row;
-            const int place = s->place[row] - base;
-            const bool mine = place >= 0 && place < n;
+            const int i = quarter * 32 + lane;
+            const bool mine = i < item.len;
+            const int m = row0 + (mine ? item.row(i) : 0);
+            if (item.box() || !ok) {
+                it += kb1 - kb0;
+            } else {
+                const int passes = (item.len + 15) / 16;
+                if (passes > 4) ok = x_rows<8>(*s, p, smem, item, row0, kb0, kb1, it);
+                else if (passes > 2) ok = x_rows<4>(*s, p, smem, item, row0, kb0, kb1, it);
+                else if (passes > 1) ok = x_rows<2>(*s, p, smem, item, row0, kb0, kb1, it);
+                else ok = x_rows<1>(*s, p, smem, item, row0, kb0, kb1, it);
+            }
             if (ok) ok = mbar_wait_warp(&s->tmem_full, turn & 1u, abort_flag);
             if (ok) {
                 tc_fence_after();
                 const float sa = mine ? __ldg(p.s_a + m) : 1.0f;
-                for (int i = 0; i < n; ++i) {
-                    if (!__any_sync(0xFFFFFFFFu, place == i)) continue;
-                    for (int c = 0; c < p.R; c += 16) {
-                        uint32_t acc[16];
-                        tmem_ld_32x32b_x16(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
-                                               static_cast<uint32_t>(i * p.Rn + c),
-                                           acc);
-                        tmem_ld_wait();
-                        if (place == i) {
+                for (int c = 0; quarter * 32 < item.len && c < p.R; c += 16) {
+                    uint32_t acc[16];
+                    __syncwarp();
+                    tmem_ld_32x32b_x16(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(c), acc);
+                    tmem_ld_wait();
+                    if (!mine) continue;
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {  // R % 8 == 0
-                                if (c + 8 * h >= p.R) continue;
-                                float f[8];
+                    for (int h = 0; h < 2; ++h) {  // R % 8 == 0
+                        if (c + 8 * h >= p.R) continue;
+                        float f[8];
 #pragma unroll
-                                for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(acc[8 * h + j]);
-                                if (p.splits > 1) {
-                                    // 16-byte units of a row rotated by the row, so that a warp's rows spread over the banks
-                                    const int units = p.R / 4;
-                                    float4* dst = reinterpret_cast<float4*>(part + row * p.R);
-                                    dst[((c + 8 * h) / 4 + row) % units] = make_float4(f[0], f[1], f[2], f[3]);
-                                    dst[((c + 8 * h) / 4 + 1 + row) % units] = make_float4(f[4], f[5], f[6], f[7]);
-                                } else {
+                        for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(acc[8 * h + j]);
+                        if (p.splits > 1) {
+                            // 16-byte units of a row rotated by the row, so that a warp's rows spread over the banks
+                            const int units = p.R / 4;
+                            float4* dst = reinterpret_cast<float4*>(part + i * p.R);
+                            dst[((c + 8 * h) / 4 + i) % units] = make_float4(f[0], f[1], f[2], f[3]);
+                            dst[((c + 8 * h) / 4 + 1 + i) % units] = make_float4(f[4], f[5], f[6], f[7]);
+                        } else {
 #pragma unroll
-                                    for (int j = 0; j < 8; ++j) f[j] = __fdiv_rn(f[j], sa);
-                                    *reinterpret_cast<uint4*>(p.t + static_cast<int64_t>(m) * p.R + c + 8 * h) =
-                                        make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]),
-                                                   pack2(f[6], f[7]));
-                                }
-                            }
+                            for (int j = 0; j < 8; ++j) f[j] = __fdiv_rn(f[j], sa);
+                            *reinterpret_cast<uint4*>(p.t + static_cast<int64_t>(m) * p.R + c + 8 * h) =
+                                make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
                         }
                     }
                 }
@@ -257,17 +449,20 @@ __global__ void __launch_bounds__(kShrinkThreads)
             if (warp >= 2) {
                 const int share = 128 / p.splits, units = p.R / 4;
                 for (int e = threadIdx.x - 64; e < share * units; e += 128) {
-                    const int row = rank * share + e / units, u = e % units;
-                    const int place = s->place[row] - base;
-                    if (place < 0 || place >= n) continue;
-                    const uint32_t at = smem_u32(reinterpret_cast<float4*>(part + row * p.R) + (u + row) % units);
-                    float4 v = ld_cluster_v4(mapa_shared(at, 0));
-                    for (int q = 1; q < p.splits; ++q) {
-                        const float4 w = ld_cluster_v4(mapa_shared(at, q));
-                        v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
-                    }
-                    const float sa = __ldg(p.s_a + row0 + row);
-                    *reinterpret_cast<uint2*>(p.t + static_cast<int64_t>(row0 + row) * p.R + 4 * u) =
+                    const int i = rank * share + e / units, u = e % units;
+                    if (i >= item.len) break;
+                    const uint32_t at = smem_u32(reinterpret_cast<float4*>(part + i * p.R) + (u + i) % units);
+                    float4 w[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        if (q < p.splits) w[q] = ld_cluster_v4(mapa_shared(at, q));
+                    float4 v = w[0];
+#pragma unroll
+                    for (int q = 1; q < 8; ++q)
+                        if (q < p.splits) v = make_float4(v.x + w[q].x, v.y + w[q].y, v.z + w[q].z, v.w + w[q].w);
+                    const int m = row0 + item.row(i);
+                    const float sa = __ldg(p.s_a + m);
+                    *reinterpret_cast<uint2*>(p.t + static_cast<int64_t>(m) * p.R + 4 * u) =
                         make_uint2(pack2(__fdiv_rn(v.x, sa), __fdiv_rn(v.y, sa)),
                                    pack2(__fdiv_rn(v.z, sa), __fdiv_rn(v.w, sa)));
                 }
@@ -599,21 +794,30 @@ tfq_status launch_shrink(const LoraCall& l, const float* s_a, int64_t M, int64_t
     a.R = l.R;
     a.Rn = (l.R + 15) / 16 * 16;
     a.n_adapters = l.n_adapters;
-    a.per_pass = std::max(1, std::min(128 / a.Rn, std::min(l.n_adapters, 128)));
     a.k_blocks = static_cast<int>((K + 63) / 64);
+    a.K = static_cast<int>(K);
+    a.x = static_cast<const __nv_bfloat16*>(l.x);
     a.idx = l.idx;
     a.s_a = s_a;
     a.t = t;
     a.err = ds->err_word;
-    const int tiles = static_cast<int>((M + 127) / 128);
-    // K over a cluster while that leaves every CTA four steps and the grid
-    // within two CTAs per SM; then the passes of tiles with many adapters
+    const int blocks = static_cast<int>((M + kShrinkRows - 1) / kShrinkRows);
+    // A CTA per 128 rows, more where rows of many adapters make more items and
+    // the grid is small; K over a cluster while every CTA keeps four steps.
+    // All of them are resident at once, two per SM.
+    const int block_rows = static_cast<int>(std::min<int64_t>(M, kShrinkRows));
+    const int least = (block_rows + 127) / 128;
+    const int items = std::min(block_rows, least + l.n_adapters - 1);
     a.splits = 1;
-    while (a.splits < 8 && tiles * a.splits * 2 <= 2 * ds->sm_count && a.k_blocks >= a.splits * 8) a.splits *= 2;
-    const int passes = (std::min(l.n_adapters, 128) + a.per_pass - 1) / a.per_pass;
-    a.pass_ctas = std::max(1, std::min(passes, 2 * ds->sm_count / (tiles * a.splits)));
-    const int stage = shrink_stage_bytes(a.per_pass * a.Rn);
-    const int rest = 1024 + static_cast<int>(sizeof(ShrinkTail)) + (a.splits > 1 ? 128 * a.R * 4 : 0);
+    while (a.splits < 8 && blocks * least * a.splits * 2 <= 2 * ds->sm_count && a.k_blocks >= a.splits * 8)
+        a.splits *= 2;
+    a.item_ctas = std::max(least, std::min(items, 2 * ds->sm_count / (a.splits * blocks)));
+    const int stage = shrink_stage_bytes(a.Rn);
+    int rest = 1024 + static_cast<int>(sizeof(ShrinkTail)) + (a.splits > 1 ? 128 * a.R * 4 : 0);
+    if (rest + 2 * stage > 227 * 1024) {  // the largest rank: no room for partial sums
+        a.splits = 1;
+        rest = 1024 + static_cast<int>(sizeof(ShrinkTail));
+    }
     // two CTAs per SM where two stages fit half the shared memory
     const int budget = rest + 2 * stage <= 112 * 1024 ? 112 * 1024 : 227 * 1024;
     a.stages = std::min(kShrinkMaxStages, (budget - rest) / stage);
@@ -632,7 +836,7 @@ tfq_status launch_shrink(const LoraCall& l, const float* s_a, int64_t M, int64_t
                                   static_cast<uint64_t>(l.n_adapters) * l.R, K * 2, 64, a.Rn,
                                   CU_TENSOR_MAP_SWIZZLE_128B);
     if (st != TFQ_OK) return st;
-    return lora_launch_error(launch_cluster(lora_shrink_kernel, static_cast<unsigned>(tiles * a.pass_ctas * a.splits),
+    return lora_launch_error(launch_cluster(lora_shrink_kernel, static_cast<unsigned>(blocks * a.item_ctas * a.splits),
                                             kShrinkThreads, smem, a.splits, stream, tmX, tmA, a));
 }
 

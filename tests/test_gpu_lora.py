@@ -76,6 +76,7 @@ CASES = [  # M, N, K, R, adapters
     (300, 520, 1024, 256, 4), (511, 328, 784, 72, 6), (512, 256, 512, 64, 2), (600, 1032, 528, 16, 9),
     (1025, 776, 2064, 64, 33), (2500, 520, 1040, 200, 5), (4111, 264, 272, 24, 100),
     (9000, 2056, 272, 24, 6), (5000, 4104, 784, 72, 3), (33, 24, 16, 8, 2), (48, 13824, 512, 256, 5),
+    (1300, 64, 144, 8, 1000), (70, 72, 4096, 256, 3), (513, 328, 2064, 248, 70),
 ]
 
 
