@@ -345,9 +345,10 @@ TFQ_API tfq_status tfq_layer_norm(const void *x, int64_t x_stride, int dtype, co
  * input: with y the fp32 value of the formula above (not rounded to `dtype`),
  *   s[m] = fl32(max(max_k |y[m,k]|, 1e-12f) / qmax),  q[m,k] = cast_E4M3FN(clamp(y[m,k] / s[m], -qmax, qmax)).
  *   q_e4m3 : [M, K] bytes, s : [M] fp32, 16-byte aligned, written.
- * The codes are those of the fp32 norm, so they can differ in the last place
- * from tfq_quant_act_fp8_per_token's on a bf16 norm output, which carries one
- * rounding more.
+ * The codes are those of the fp32 norm (not of its bf16 rounding, as the norm
+ * and tfq_quant_act_fp8_per_token in two calls would give); y / s is formed in
+ * fp32 to within 2 ulp, so a quotient that close to the middle of two codes
+ * may take either.
  * M == 0 is a no-op; K == 0 writes s only.
  * Errors as tfq_layer_norm, and TFQ_EINVAL for K % 16 != 0, qmax outside
  * [1, 448] or an output that is not 16-byte aligned.

@@ -19,6 +19,7 @@ enum : uint32_t {
     kErrGemmDrain = 1u << 7,
     kErrSelfTest = 1u << 8,
     kErrQuantStage = 1u << 9,  // a staged-row quantizer gave up waiting for a row load
+    kErrNorm = 1u << 11,       // a layer norm gave up waiting for a row
     kErrLora = 1u << 10,       // the adapters' first product gave up
 };
 
@@ -40,6 +41,7 @@ struct DeviceState {
     bool gemm_attr_set[6] = {false, false, false, false, false, false};
     bool lora_attr_set = false;    // the CTA-pair GEMM with low-rank adapters
     bool shrink_attr_set = false;  // the adapters' first product
+    bool norm_attr_set = false;    // the layer norms' row rings
     bool small_attr_set = false;   // the Linear with adapters for few rows
     bool quant_attr_set = false;   // dynamic shared memory limit of the staged-row quantizers
 };

@@ -18,12 +18,15 @@
 // variance is summed from x - mean (two passes over a row that stays in
 // registers), so a large common offset costs no digits.
 //
-// Bound by HBM: a row is read once into registers.  A row belongs to `tpr`
-// threads: a power of two up to 32 (several rows per warp, no barrier) or a
-// whole CTA of up to 1024; thread t holds the row's 16-byte units t, t + tpr,
-// ... (J at most).  CTAs walk consecutive rows and load the next row before
-// they reduce the present one.  The weight and bias are read again for every
-// row: they stay in L1 (the row loads do not allocate there).
+// Bound by HBM.  Rows of 16-byte units with 33 to 640 threads of 16 columns
+// each (K from 513 to 10240) run the ring kernels further down.  The others
+// (short rows, very long ones, rows of odd length or alignment) are read into
+// registers: a row belongs to `tpr` threads, a power of two up to 32 (several
+// rows per warp, no barrier) or a whole CTA of up to 1024; thread t holds the
+// row's units t, t + tpr, ... (J at most).  CTAs walk consecutive rows and load
+// the next row before they reduce the present one.  The weight and bias are
+// read again for every row: they stay in L1 (the row loads do not allocate
+// there).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -65,6 +68,16 @@ __device__ __forceinline__ T ldg_elem(const T* p) {
         const unsigned short w = __ldg(reinterpret_cast<const unsigned short*>(p));
         return *reinterpret_cast<const T*>(&w);
     }
+}
+
+// Four fp32 values -> four E4M3 codes, the first in the low byte.
+__device__ __forceinline__ uint32_t cvt_e4m3x4(float2 lo, float2 hi) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\t"
+        "mov.b32 %0, {a, b};\n\t}"
+        : "=r"(r)
+        : "f"(lo.x), "f"(lo.y), "f"(hi.x), "f"(hi.y));
+    return r;
 }
 
 template <typename T, int VEC>
@@ -543,6 +556,375 @@ __global__ void __launch_bounds__(256) norm_partials_kernel(const float* part_dw
     }
 }
 
+// ------------------------------------------------- rows through shared memory
+// The kernels of wide rows (16-byte units, 33 to 640 threads a row).  Thread t
+// owns 16 columns of every row (units t, t + T, ...), whose weight, bias and,
+// in the backward, gradient sums stay in its registers while the CTA walks
+// consecutive rows.  The rows themselves arrive in a ring of shared-memory
+// slots by bulk copies several rows ahead, which keeps enough bytes in flight
+// for HBM whatever the CTA is waiting for (loads into registers one row ahead
+// reached 2 TB/s on the quantizing norm of 75600 x 5120).
+//
+// The forward has one barrier per row: a warp forms the sum of its columns, its
+// own mean and the squares about that (all by shuffles); the warps' three
+// numbers are joined behind the barrier, sum (x - mean)^2 = sum over the warps
+// of M2_w + n_w (mean_w - mean)^2, which never subtracts large squares.
+// Arithmetic is on pairs (fp32x2 instructions): at some seven instructions per
+// value the quantizing form would otherwise be bound by them, not by HBM.
+constexpr int kRingCols = 16;     // columns per thread
+constexpr int kRingMaxSlots = 8;
+constexpr int kRingSmall = 320;   // threads per CTA of the variant with two CTAs' registers per SM
+constexpr int kRingLarge = 640;   // ... with one
+
+// A thread's columns as pairs; column pair i is in unit i / (VEC / 2).
+template <typename T>
+struct RingRow {
+    static constexpr int VEC = 16 / sizeof(T);
+    static constexpr int J = kRingCols / VEC;
+    static constexpr int P = kRingCols / 2;
+    __device__ static __forceinline__ void get(float2 (&f)[P], const uint8_t* slot, int t, int threads, int units) {
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int u = t + threads * j;
+            Unit<T, VEC> raw;
+            raw.clear();
+            if (u < units) raw.raw = reinterpret_cast<const uint4*>(slot)[u];
+            float v[VEC];
+            raw.get(v);
+#pragma unroll
+            for (int i = 0; i < VEC / 2; ++i) f[j * (VEC / 2) + i] = make_float2(v[2 * i], v[2 * i + 1]);
+        }
+    }
+    __device__ static __forceinline__ void put(const float2 (&f)[P], T* row, int t, int threads, int units) {
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int u = t + threads * j;
+            float v[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC / 2; ++i) {
+                v[2 * i] = f[j * (VEC / 2) + i].x;
+                v[2 * i + 1] = f[j * (VEC / 2) + i].y;
+            }
+            if (u < units) Unit<T, VEC>::store(row, u, v);
+        }
+    }
+    // Weight or bias of group g: w + offset, or `missing` without one.
+    __device__ static __forceinline__ void affine(float2 (&f)[P], const void* base, bool f32, int64_t at, float offset,
+                                                  float missing, int t, int threads, int units) {
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int u = t + threads * j;
+            float v[VEC];
+            if (base != nullptr && u < units) load_affine<T, VEC>(v, base, f32, at + static_cast<int64_t>(u) * VEC);
+#pragma unroll
+            for (int i = 0; i < VEC / 2; ++i)
+                f[j * (VEC / 2) + i] = base != nullptr && u < units ? make_float2(v[2 * i] + offset, v[2 * i + 1] + offset)
+                                                                   : make_float2(missing, missing);
+        }
+    }
+};
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+// A number per warp, zero past the CTA's warps, read whole by every thread.
+template <int kMaxThreads>
+struct PerWarp {
+    static constexpr int kQuads = (kMaxThreads / 32 + 3) / 4;
+    float4 v[kQuads];
+    __device__ __forceinline__ float& operator[](int i) { return reinterpret_cast<float*>(v)[i]; }
+    __device__ __forceinline__ float sum() const {
+        float4 q[kQuads];
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i) q[i] = v[i];
+        float2 a = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i)
+            a = __fadd2_rn(a, __fadd2_rn(make_float2(q[i].x, q[i].y), make_float2(q[i].z, q[i].w)));
+        return a.x + a.y;
+    }
+    __device__ __forceinline__ float max() const {  // of values >= 0
+        float4 q[kQuads];
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i) q[i] = v[i];
+        float m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i) m = fmaxf(m, fmaxf(fmaxf(q[i].x, q[i].y), fmaxf(q[i].z, q[i].w)));
+        return m;
+    }
+};
+
+template <int kMaxThreads>
+struct RingShared {
+    PerWarp<kMaxThreads> sum[2], m2[2], amax, count, inv_count;  // count: a warp's columns
+    uint64_t full[kRingMaxSlots];
+    // sum over the warps of m2 + count (sum / count - mean)^2
+    __device__ __forceinline__ float squares(int par, float mean) const {
+        float2 a = make_float2(0.0f, 0.0f);
+        const float2 neg = make_float2(-mean, -mean);
+#pragma unroll
+        for (int i = 0; i < PerWarp<kMaxThreads>::kQuads; ++i) {
+            const float4 q = sum[par].v[i], n = count.v[i], r = inv_count.v[i], m = m2[par].v[i];
+            const float2 d0 = __ffma2_rn(make_float2(q.x, q.y), make_float2(r.x, r.y), neg);
+            const float2 d1 = __ffma2_rn(make_float2(q.z, q.w), make_float2(r.z, r.w), neg);
+            a = __fadd2_rn(a, __ffma2_rn(__fmul2_rn(make_float2(n.x, n.y), d0), d0, make_float2(m.x, m.y)));
+            a = __fadd2_rn(a, __ffma2_rn(__fmul2_rn(make_float2(n.z, n.w), d1), d1, make_float2(m.z, m.w)));
+        }
+        return a.x + a.y;
+    }
+};
+
+// kMode: 0 = values out, 1 = codes, 2 = codes of values clamped to +-qmax first
+// (qmax is not an E4M3 value).
+template <typename T, int kMode, int kMaxThreads>
+__global__ void __launch_bounds__(kMaxThreads, kMaxThreads <= kRingSmall ? 2 : 1)
+    norm_ring_kernel(const NormArgs p, int slots, uint32_t* err) {
+    using Row = RingRow<T>;
+    constexpr int P = Row::P, VEC = Row::VEC, J = Row::J;
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ RingShared<kMaxThreads> s;
+    const int t = threadIdx.x, threads = blockDim.x, warp = t >> 5, lane = t & 31;
+    const int units = p.K / VEC;
+    const uint32_t row_bytes = static_cast<uint32_t>(p.K * sizeof(T));
+    if (t == 0) {
+        for (int i = 0; i < slots; ++i) mbar_init(&s.full[i], 1);
+        fence_mbar_init();
+    }
+    int mine = 0;
+    bool valid[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        valid[j] = t + threads * j < units;
+        mine += valid[j] ? VEC : 0;
+    }
+    const float n_warp = warp_sum(static_cast<float>(mine));
+    const float inv_n_warp = n_warp > 0.0f ? 1.0f / n_warp : 0.0f;
+    if (t < 4 * PerWarp<kMaxThreads>::kQuads) {
+        s.sum[0][t] = s.sum[1][t] = s.m2[0][t] = s.m2[1][t] = 0.0f;
+        s.amax[t] = s.count[t] = s.inv_count[t] = 0.0f;
+    }
+    __syncthreads();
+    if (lane == 0) {
+        s.count[warp] = n_warp;
+        s.inv_count[warp] = inv_n_warp;
+    }
+    __syncthreads();
+    pdl_allow_next();
+    pdl_wait();
+    const int64_t chunk = (p.M + gridDim.x - 1) / gridDim.x;
+    const int64_t first = blockIdx.x * chunk;
+    const int64_t last = min(p.M, first + chunk);
+    const auto fetch = [&](int64_t r, int slot) {
+        mbar_arrive_expect_tx(&s.full[slot], row_bytes);
+        bulk_g2s(ring + static_cast<size_t>(slot) * row_bytes, static_cast<const T*>(p.x) + r * p.x_stride, row_bytes,
+                 &s.full[slot]);
+    };
+    if (t == 0)
+        for (int i = 0; i < slots && first + i < last; ++i) fetch(first + i, i);
+    const float inv_k = 1.0f / static_cast<float>(p.K);
+    int64_t group = -1;
+    float2 w[P], b[P];
+    int slot = 0;
+    uint32_t phase = 0;
+    for (int64_t r = first; r < last; ++r) {
+        const int64_t g = p.group_rows == p.M ? 0 : static_cast<uint32_t>(r) / static_cast<uint32_t>(p.group_rows);
+        if (g != group) {
+            group = g;
+            Row::affine(w, p.w, p.w_f32, g * p.K, p.offset, 1.0f, t, threads, units);
+            Row::affine(b, p.b, p.w_f32, g * p.K, 0.0f, 0.0f, t, threads, units);
+#pragma unroll
+            for (int i = 0; i < P; ++i)  // a column past the row gives 0, which no maximum sees
+                if (!valid[i / (VEC / 2)]) w[i] = make_float2(0.0f, 0.0f);
+        }
+        if (!mbar_wait(&s.full[slot], phase, nullptr)) {
+            atomicOr(err, kErrNorm);
+            break;
+        }
+        float2 x[P];
+        Row::get(x, ring + static_cast<size_t>(slot) * row_bytes, t, threads, units);
+        float2 acc = x[0];
+#pragma unroll
+        for (int i = 1; i < P; ++i) acc = __fadd2_rn(acc, x[i]);
+        const float sum_w = warp_sum(acc.x + acc.y);
+        const float mean_w = sum_w * inv_n_warp;
+        acc = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const float2 d = __fadd2_rn(x[i], make_float2(-mean_w, -mean_w));
+            if (valid[i / (VEC / 2)]) acc = __ffma2_rn(d, d, acc);
+        }
+        const float m2_w = warp_sum(acc.x + acc.y);
+        const int par = static_cast<int>(r & 1);
+        if (lane == 0) {
+            s.sum[par][warp] = sum_w;
+            s.m2[par][warp] = m2_w;
+        }
+        __syncthreads();
+        // every thread has its columns: the slot takes the row `slots` further on
+        if (t == 0 && r + slots < last) fetch(r + slots, slot);
+        const float mean = s.sum[par].sum() * inv_k;
+        const float rstd = rsqrtf(fmaf(s.squares(par, mean), inv_k, p.eps));
+        if (p.mean != nullptr && t == 0) {
+            p.mean[r] = mean;
+            p.rstd[r] = rstd;
+        }
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const float2 xhat = __fmul2_rn(__fadd2_rn(x[i], make_float2(-mean, -mean)), make_float2(rstd, rstd));
+            x[i] = __ffma2_rn(xhat, w[i], b[i]);
+        }
+        if constexpr (kMode == 0) {
+            Row::put(x, static_cast<T*>(p.y) + r * p.K, t, threads, units);
+        } else {
+            float m = 0.0f;
+#pragma unroll
+            for (int i = 0; i < P; ++i) m = fmaxf(m, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
+            // non-negative floats compare as their bits do
+            const uint32_t m_w = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(m));
+            if (lane == 0) s.amax[warp] = __uint_as_float(m_w);
+            __syncthreads();
+            const float sc = __fdiv_rn(fmaxf(s.amax.max(), 1e-12f), p.qmax);
+            if (t == 0) p.s[r] = sc;
+            float rcp;  // 1 ulp; with the product's half the quotient is good to 1.5
+            asm("rcp.approx.f32 %0, %1;" : "=f"(rcp) : "f"(sc));
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                x[i] = __fmul2_rn(x[i], make_float2(rcp, rcp));
+                if constexpr (kMode == 2) {
+                    x[i].x = fminf(fmaxf(x[i].x, -p.qmax), p.qmax);
+                    x[i].y = fminf(fmaxf(x[i].y, -p.qmax), p.qmax);
+                }
+            }
+            uint8_t* out = p.q + r * p.K;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const int u = t + threads * j;
+                uint32_t c[VEC / 4];
+#pragma unroll
+                for (int i = 0; i < VEC / 4; ++i) {
+                    const float2 lo = x[j * (VEC / 2) + 2 * i], hi = x[j * (VEC / 2) + 2 * i + 1];
+                    c[i] = cvt_e4m3x4(lo, hi);
+                }
+                if (valid[j]) {
+                    if constexpr (VEC == 8) reinterpret_cast<uint2*>(out)[u] = make_uint2(c[0], c[1]);
+                    else reinterpret_cast<uint32_t*>(out)[u] = c[0];
+                }
+            }
+        }
+        if (++slot == slots) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
+}
+
+// Backward through the ring (a slot holds a row of x, then its row of dy); grid
+// and partial sums as in norm_backward_kernel.
+template <typename T, int kMaxThreads>
+__global__ void __launch_bounds__(kMaxThreads, kMaxThreads <= kRingSmall ? 2 : 1)
+    norm_backward_ring_kernel(const NormArgs p, int slots, uint32_t* err) {
+    using Row = RingRow<T>;
+    constexpr int P = Row::P, VEC = Row::VEC, J = Row::J;
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ uint64_t full[kRingMaxSlots];
+    __shared__ PerWarp<kMaxThreads> sums[2][2];
+    const int t = threadIdx.x, threads = blockDim.x, warp = t >> 5, lane = t & 31;
+    const int units = p.K / VEC;
+    const uint32_t row_bytes = static_cast<uint32_t>(p.K * sizeof(T));
+    if (t == 0) {
+        for (int i = 0; i < slots; ++i) mbar_init(&full[i], 1);
+        fence_mbar_init();
+    }
+    if (t < 4 * PerWarp<kMaxThreads>::kQuads) sums[0][0][t] = sums[0][1][t] = sums[1][0][t] = sums[1][1][t] = 0.0f;
+    __syncthreads();
+    pdl_allow_next();
+    pdl_wait();
+    const int64_t g = blockIdx.x / static_cast<unsigned>(p.parts);
+    const int64_t part = blockIdx.x % static_cast<unsigned>(p.parts);
+    const int64_t chunk = (p.group_rows + p.parts - 1) / p.parts;
+    const int64_t first = g * p.group_rows + part * chunk;
+    const int64_t last = min((g + 1) * p.group_rows, first + chunk);
+    const auto fetch = [&](int64_t r, int slot) {
+        mbar_arrive_expect_tx(&full[slot], 2 * row_bytes);
+        uint8_t* dst = ring + static_cast<size_t>(slot) * 2 * row_bytes;
+        bulk_g2s(dst, static_cast<const T*>(p.x) + r * p.x_stride, row_bytes, &full[slot]);
+        bulk_g2s(dst + row_bytes, static_cast<const T*>(p.dy) + r * p.dy_stride, row_bytes, &full[slot]);
+    };
+    if (t == 0)
+        for (int i = 0; i < slots && first + i < last; ++i) fetch(first + i, i);
+    const float inv_k = 1.0f / static_cast<float>(p.K);
+    float2 w[P], dw[P], db[P];
+    Row::affine(w, p.w, p.w_f32, g * p.K, p.offset, 1.0f, t, threads, units);
+#pragma unroll
+    for (int i = 0; i < P; ++i) dw[i] = db[i] = make_float2(0.0f, 0.0f);
+    float mean = first < last ? __ldg(p.mean + first) : 0.0f, rstd = first < last ? __ldg(p.rstd + first) : 0.0f;
+    int slot = 0;
+    uint32_t phase = 0;
+    for (int64_t r = first; r < last; ++r) {
+        const float next_mean = r + 1 < last ? __ldg(p.mean + r + 1) : 0.0f;
+        const float next_rstd = r + 1 < last ? __ldg(p.rstd + r + 1) : 0.0f;
+        if (!mbar_wait(&full[slot], phase, nullptr)) {
+            atomicOr(err, kErrNorm);
+            break;
+        }
+        const uint8_t* src = ring + static_cast<size_t>(slot) * 2 * row_bytes;
+        float2 xhat[P], h[P];
+        Row::get(xhat, src, t, threads, units);
+        Row::get(h, src + row_bytes, t, threads, units);
+        float2 s1 = make_float2(0.0f, 0.0f), s2 = s1;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {  // past the row dy is 0, and so is h
+            xhat[i] = __fmul2_rn(__fadd2_rn(xhat[i], make_float2(-mean, -mean)), make_float2(rstd, rstd));
+            dw[i] = __ffma2_rn(h[i], xhat[i], dw[i]);
+            db[i] = __fadd2_rn(db[i], h[i]);
+            h[i] = __fmul2_rn(h[i], w[i]);
+            s1 = __fadd2_rn(s1, h[i]);
+            s2 = __ffma2_rn(h[i], xhat[i], s2);
+        }
+        const float a1 = warp_sum(s1.x + s1.y), a2 = warp_sum(s2.x + s2.y);
+        const int par = static_cast<int>(r & 1);
+        if (lane == 0) {
+            sums[par][0][warp] = a1;
+            sums[par][1][warp] = a2;
+        }
+        __syncthreads();
+        if (t == 0 && r + slots < last) fetch(r + slots, slot);
+        if (p.dx != nullptr) {
+            const float c1 = sums[par][0].sum() * inv_k, c2 = sums[par][1].sum() * inv_k;
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const float2 e = __ffma2_rn(xhat[i], make_float2(-c2, -c2), __fadd2_rn(h[i], make_float2(-c1, -c1)));
+                h[i] = __fmul2_rn(e, make_float2(rstd, rstd));
+            }
+            Row::put(h, static_cast<T*>(p.dx) + r * p.K, t, threads, units);
+        }
+        mean = next_mean;
+        rstd = next_rstd;
+        if (++slot == slots) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
+    const int64_t out = (g * p.parts + part) * p.K;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const int u = t + threads * j;
+        if (u >= units) continue;
+#pragma unroll
+        for (int i = 0; i < VEC / 4; ++i) {
+            const float2 lo = dw[j * (VEC / 2) + 2 * i], hi = dw[j * (VEC / 2) + 2 * i + 1];
+            if (p.part_dw != nullptr)
+                reinterpret_cast<float4*>(p.part_dw + out)[u * (VEC / 4) + i] = make_float4(lo.x, lo.y, hi.x, hi.y);
+            const float2 lo2 = db[j * (VEC / 2) + 2 * i], hi2 = db[j * (VEC / 2) + 2 * i + 1];
+            if (p.part_db != nullptr)
+                reinterpret_cast<float4*>(p.part_db + out)[u * (VEC / 4) + i] = make_float4(lo2.x, lo2.y, hi2.x, hi2.y);
+        }
+    }
+}
+
 // ------------------------------------------------- launch shapes
 struct NormShape {
     bool vec;   // 16-byte units
@@ -574,6 +956,25 @@ tfq_status launch_error(const char* what, cudaError_t e) {
 }
 
 using NormKernel = void (*)(const NormArgs);
+using RingKernel = void (*)(const NormArgs, int, uint32_t*);
+
+// The ring kernels' shape for rows of K elements (0 threads: not for them).
+struct RingShape {
+    int threads;
+    int per_sm;  // CTAs per SM by registers
+    int slots;
+    size_t smem;
+};
+
+RingShape ring_shape(int64_t K, int elem, bool vec, int rows_per_slot) {
+    const int threads = static_cast<int>((K + kRingCols - 1) / kRingCols + 31) / 32 * 32;
+    if (!vec || threads <= 32 || threads > kRingLarge) return {0, 0, 0, 0};
+    const int64_t slot = K * elem * rows_per_slot;
+    const int per_sm = std::min(8, std::max(1, 21 / (threads / 32)));  // at 96 registers 21 warps fit
+    // about 96 KB of rows in flight per SM
+    const int slots = static_cast<int>(std::max<int64_t>(2, std::min<int64_t>(kRingMaxSlots, 96 * 1024 / (slot * per_sm))));
+    return {threads, per_sm, slots, static_cast<size_t>(slot * slots)};
+}
 
 template <typename T, bool kQuant>
 NormKernel forward_kernel(const NormShape& s) {
@@ -601,6 +1002,40 @@ NormKernel backward_kernel(const NormShape& s) {
     if (s.block == 256 && s.tpr <= 32) return norm_backward_kernel<T, 1, 2, true>;
     if (s.j == 2) return norm_backward_kernel<T, 1, 2, false>;
     return s.j == 8 ? norm_backward_kernel<T, 1, 8, false> : norm_backward_kernel<T, 1, 32, false>;
+}
+
+template <typename T>
+RingKernel ring_forward(bool quant, bool clamp, bool small) {
+    if (clamp) return small ? norm_ring_kernel<T, 2, kRingSmall> : norm_ring_kernel<T, 2, kRingLarge>;
+    if (quant) return small ? norm_ring_kernel<T, 1, kRingSmall> : norm_ring_kernel<T, 1, kRingLarge>;
+    return small ? norm_ring_kernel<T, 0, kRingSmall> : norm_ring_kernel<T, 0, kRingLarge>;
+}
+template <typename T>
+RingKernel ring_backward(bool small) {
+    return small ? norm_backward_ring_kernel<T, kRingSmall> : norm_backward_ring_kernel<T, kRingLarge>;
+}
+
+// Opt-in shared memory of the ring kernels (once per device).
+constexpr int kRingSmem = 160 * 1024;
+template <typename T>
+cudaError_t ring_attributes_of() {
+    cudaError_t e = cudaSuccess;
+    for (bool small : {true, false}) {
+        const RingKernel k[4] = {ring_forward<T>(false, false, small), ring_forward<T>(true, false, small),
+                                 ring_forward<T>(true, true, small), ring_backward<T>(small)};
+        for (RingKernel f : k)
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
+    }
+    return e;
+}
+tfq_status ring_attributes(DeviceState* ds) {
+    if (ds->norm_attr_set) return TFQ_OK;
+    cudaError_t e = ring_attributes_of<float>();
+    if (e == cudaSuccess) e = ring_attributes_of<__half>();
+    if (e == cudaSuccess) e = ring_attributes_of<__nv_bfloat16>();
+    if (e != cudaSuccess) return fail(TFQ_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    ds->norm_attr_set = true;
+    return TFQ_OK;
 }
 
 int elem_size(int dtype) { return dtype == TFQ_DTYPE_FP32 ? 4 : 2; }
@@ -651,6 +1086,19 @@ tfq_status launch_layer_norm(const NormCall& c, void* y, uint8_t* q, float* s, f
     a.s = s;
     a.qmax = qmax;
     a.clamp = q != nullptr && !is_e4m3_value(qmax);
+    const RingShape ring = ring_shape(c.K, e, sh.vec, 1);
+    if (ring.threads > 0) {
+        const bool small = ring.threads <= kRingSmall;
+        RingKernel rk;
+        if (c.dtype == TFQ_DTYPE_FP32) rk = ring_forward<float>(q != nullptr, a.clamp != 0, small);
+        else if (c.dtype == TFQ_DTYPE_FP16) rk = ring_forward<__half>(q != nullptr, a.clamp != 0, small);
+        else rk = ring_forward<__nv_bfloat16>(q != nullptr, a.clamp != 0, small);
+        const tfq_status st = ring_attributes(ds);
+        if (st != TFQ_OK) return st;
+        const int64_t grid = std::min<int64_t>(c.M, static_cast<int64_t>(ds->sm_count) * ring.per_sm);
+        return launch_error("layer norm", launch_kernel(rk, dim3(static_cast<unsigned>(grid)), dim3(ring.threads),
+                                                        ring.smem, stream, a, ring.slots, ds->err_word));
+    }
     NormKernel k;
     if (c.dtype == TFQ_DTYPE_FP32) k = q ? forward_kernel<float, true>(sh) : forward_kernel<float, false>(sh);
     else if (c.dtype == TFQ_DTYPE_FP16) k = q ? forward_kernel<__half, true>(sh) : forward_kernel<__half, false>(sh);
@@ -662,17 +1110,19 @@ tfq_status launch_layer_norm(const NormCall& c, void* y, uint8_t* q, float* s, f
 // Row shares per group of the backward: enough CTAs to fill the GPU once, each
 // with rows for every slot of the CTA.
 constexpr int kNormMaxSms = 160;  // the workspace formula knows no device: more SMs add no parts
-static int64_t backward_parts(int64_t M, int64_t groups, const NormShape& s, int sm_count) {
-    const int64_t slots = s.block / s.tpr;
-    const int64_t ctas = static_cast<int64_t>(std::min(sm_count, kNormMaxSms)) * std::max(1, std::min(8, 1024 / s.block));
+static int64_t backward_parts(int64_t M, int64_t K, int64_t groups, int elem, bool vec, int sm_count) {
+    const NormShape s = norm_shape(K, elem, vec);
+    const RingShape ring = ring_shape(K, elem, vec, 2);
+    const int64_t slots = ring.threads > 0 ? 1 : s.block / s.tpr;
+    const int per_sm = ring.threads > 0 ? ring.per_sm : std::max(1, std::min(8, 1024 / s.block));
+    const int64_t ctas = static_cast<int64_t>(std::min(sm_count, kNormMaxSms)) * per_sm;
     return std::max<int64_t>(1, std::min<int64_t>((M / groups + slots - 1) / slots, (ctas + groups - 1) / groups));
 }
 
 int64_t layer_norm_backward_workspace(int64_t M, int64_t K, int64_t groups) {
     int64_t parts = 1;  // the most that any type and alignment of the operands takes
     for (int e : {2, 4})
-        for (bool vec : {true, false})
-            parts = std::max(parts, backward_parts(M, groups, norm_shape(K, e, vec), kNormMaxSms));
+        for (bool vec : {true, false}) parts = std::max(parts, backward_parts(M, K, groups, e, vec, kNormMaxSms));
     return 2 * groups * parts * K * 4;
 }
 
@@ -685,14 +1135,26 @@ tfq_status launch_layer_norm_backward(const NormCall& c, const void* dy, int64_t
     a.dy = dy;
     a.dy_stride = dy_stride;
     a.dx = dx;
-    a.parts = static_cast<int>(backward_parts(c.M, c.groups, sh, ds->sm_count));
+    const RingShape ring = ring_shape(c.K, e, vec, 2);
+    a.parts = static_cast<int>(backward_parts(c.M, c.K, c.groups, e, vec, ds->sm_count));
     const int64_t n = c.groups * a.parts * c.K;
     a.part_dw = dw != nullptr ? workspace : nullptr;
     a.part_db = db != nullptr ? workspace + (dw != nullptr ? n : 0) : nullptr;
-    NormKernel k = c.dtype == TFQ_DTYPE_FP32 ? backward_kernel<float>(sh)
-                   : c.dtype == TFQ_DTYPE_FP16 ? backward_kernel<__half>(sh) : backward_kernel<__nv_bfloat16>(sh);
     const dim3 grid(static_cast<unsigned>(a.parts * c.groups));
-    tfq_status st = launch_error("layer norm backward", launch_kernel(k, grid, dim3(sh.block), 0, stream, a));
+    tfq_status st;
+    if (ring.threads > 0) {
+        const bool small = ring.threads <= kRingSmall;
+        RingKernel rk = c.dtype == TFQ_DTYPE_FP32 ? ring_backward<float>(small)
+                        : c.dtype == TFQ_DTYPE_FP16 ? ring_backward<__half>(small) : ring_backward<__nv_bfloat16>(small);
+        st = ring_attributes(ds);
+        if (st != TFQ_OK) return st;
+        st = launch_error("layer norm backward", launch_kernel(rk, grid, dim3(ring.threads), ring.smem, stream, a,
+                                                               ring.slots, ds->err_word));
+    } else {
+        NormKernel k = c.dtype == TFQ_DTYPE_FP32 ? backward_kernel<float>(sh)
+                       : c.dtype == TFQ_DTYPE_FP16 ? backward_kernel<__half>(sh) : backward_kernel<__nv_bfloat16>(sh);
+        st = launch_error("layer norm backward", launch_kernel(k, grid, dim3(sh.block), 0, stream, a));
+    }
     if (st != TFQ_OK || (dw == nullptr && db == nullptr)) return st;
     auto join = c.dtype == TFQ_DTYPE_FP32 ? norm_partials_kernel<float>
                 : c.dtype == TFQ_DTYPE_FP16 ? norm_partials_kernel<__half> : norm_partials_kernel<__nv_bfloat16>;

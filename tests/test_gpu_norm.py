@@ -80,7 +80,7 @@ def guard(shape, dtype, fill=77.0):
 
 SHAPES = [(1, 1), (1, 16), (3, 8), (5, 7), (33, 64), (300, 128), (7, 130), (64, 512), (2, 1001), (130, 1024),
           (9, 1536), (6, 2048), (5, 5120), (3, 8192), (3, 8200), (2, 12288), (2, 13824), (1, 32768), (2, 32767),
-          (1200, 96)]
+          (1200, 96), (700, 520), (33, 640), (2, 10240), (2, 10256), (400, 1040), (1300, 5120)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
@@ -131,7 +131,8 @@ def e4m3_spacing(v):
 @pytest.mark.parametrize("qmax", [448.0, 14.0, 7.0, 100.3])
 @pytest.mark.parametrize("M,K,dtype", [(1, 16, "bf16"), (37, 64, "fp16"), (9, 144, "fp32"), (70, 1024, "bf16"),
                                        (5, 5120, "bf16"), (4, 5120, "fp32"), (3, 13824, "bf16"), (2, 32768, "bf16"),
-                                       (2, 32768, "fp32"), (600, 256, "bf16")])
+                                       (2, 32768, "fp32"), (600, 256, "bf16"), (700, 528, "fp16"),
+                                       (33, 640, "fp32"), (2, 10240, "fp32"), (1300, 5120, "bf16")])
 def test_quant(M, K, dtype, qmax):
     seed = M + K
     pad = (0, 3, 8)[seed % 3]
@@ -185,7 +186,8 @@ def test_large_offset_keeps_its_digits():
 
 BWD_SHAPES = [(1, 1, 1), (1, 16, 1), (6, 8, 3), (5, 7, 1), (33, 64, 1), (300, 128, 2), (7, 130, 1), (700, 512, 1),
               (2, 1001, 1), (517, 1001, 1), (130, 1024, 1), (40, 1536, 4), (900, 5120, 3), (3, 8200, 1),
-              (4, 13824, 2), (2, 32768, 1), (2, 32767, 1), (1500, 96, 1), (12, 48, 12), (1300, 2048, 1)]
+              (4, 13824, 2), (2, 32768, 1), (2, 32767, 1), (1500, 96, 1), (12, 48, 12), (1300, 2048, 1), (700, 520, 7), (33, 640, 1), (2, 10240, 1),
+              (2, 10256, 1), (400, 1040, 400), (1300, 5120, 1)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
