@@ -925,6 +925,181 @@ __global__ void __launch_bounds__(kMaxThreads, kMaxThreads <= kRingSmall ? 2 : 1
     }
 }
 
+// ------------------------------------------------- one warp per row
+// Many wide rows (16-byte units, K up to 32 * 160): a warp holds a whole row as
+// fp32 pairs, C columns a lane, so that all three reductions are shuffles, no
+// barrier holds a row up and a row costs about 1000 instructions; the weight
+// (with its offset) and bias lie in shared memory as fp32, which every warp of
+// the CTA reads.  Each warp has two row slots of its own and the copy of its
+// row after next in flight.  A CTA stays within one group.  (Measured on B200,
+// 75600 x 5120 to codes: the CTA-per-row ring above 394 us, bound by
+// instructions and barriers.)
+constexpr int kWarpRows = 8;   // warps per CTA
+constexpr int kWarpSlots = 2;
+
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+    float d;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+template <typename T, bool kQuant, int C>
+__global__ void __launch_bounds__(32 * kWarpRows, C <= 64 ? 2 : 1) norm_warp_kernel(const NormArgs p, uint32_t* err) {
+    constexpr int VEC = 16 / sizeof(T), J = C / VEC, P = C / 2;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint64_t full[kWarpRows][kWarpSlots];
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    const int units = p.K / VEC;
+    const uint32_t row_bytes = static_cast<uint32_t>(p.K * sizeof(T));
+    float4* sw = reinterpret_cast<float4*>(smem);  // [K] weight + offset, then [K] bias
+    float4* sb = sw + p.K / 4;
+    uint8_t* ring = smem + 8 * static_cast<size_t>(p.K) + static_cast<size_t>(warp) * kWarpSlots * row_bytes;
+    if (lane == 0) {
+        for (int i = 0; i < kWarpSlots; ++i) mbar_init(&full[warp][i], 1);
+        fence_mbar_init();
+    }
+    pdl_allow_next();
+    pdl_wait();
+    const int64_t g = blockIdx.x / static_cast<unsigned>(p.parts);
+    const int64_t part = blockIdx.x % static_cast<unsigned>(p.parts);
+    // the group's rows, dealt to its parts * kWarpRows warps in turn
+    const int64_t first = g * p.group_rows + part * kWarpRows + warp, last = (g + 1) * p.group_rows;
+    const int64_t step = static_cast<int64_t>(p.parts) * kWarpRows;
+    __syncwarp();
+    const auto fetch = [&](int64_t r, int slot) {
+        mbar_arrive_expect_tx(&full[warp][slot], row_bytes);
+        bulk_g2s(ring + slot * row_bytes, static_cast<const T*>(p.x) + r * p.x_stride, row_bytes, &full[warp][slot]);
+    };
+    if (lane == 0)
+        for (int i = 0; i < kWarpSlots && first + i * step < last; ++i) fetch(first + i * step, i);
+    for (int c = t; c < p.K; c += 32 * kWarpRows) {
+        const int64_t at = g * p.K + c;
+        float w[1] = {1.0f}, b[1] = {0.0f};
+        if (p.w != nullptr) {
+            load_affine<T, 1>(w, p.w, p.w_f32, at);
+            w[0] += p.offset;
+        }
+        if (p.b != nullptr) load_affine<T, 1>(b, p.b, p.w_f32, at);
+        reinterpret_cast<float*>(sw)[c] = w[0];
+        reinterpret_cast<float*>(sb)[c] = b[0];
+    }
+    __syncthreads();
+    const float inv_k = 1.0f / static_cast<float>(p.K);
+    int slot = 0;
+    uint32_t phase = 0;
+    for (int64_t r = first; r < last; r += step) {
+        if (!mbar_wait(&full[warp][slot], phase, nullptr)) {
+            atomicOr(err, kErrNorm);
+            break;
+        }
+        float2 x[P];
+        const uint4* src = reinterpret_cast<const uint4*>(ring + slot * row_bytes);
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int u = lane + 32 * j;
+            Unit<T, VEC> raw;
+            raw.clear();
+            if (u < units) raw.raw = src[u];
+            float v[VEC];
+            raw.get(v);
+#pragma unroll
+            for (int i = 0; i < VEC / 2; ++i) x[j * (VEC / 2) + i] = make_float2(v[2 * i], v[2 * i + 1]);
+        }
+        __syncwarp();
+        if (lane == 0 && r + kWarpSlots * step < last) fetch(r + kWarpSlots * step, slot);
+        float2 a0 = make_float2(0.0f, 0.0f), a1 = a0, a2 = a0, a3 = a0;
+#pragma unroll
+        for (int i = 0; i < P; i += 4) {
+            a0 = __fadd2_rn(a0, x[i]);
+            a1 = __fadd2_rn(a1, x[i + 1]);
+            a2 = __fadd2_rn(a2, x[i + 2]);
+            a3 = __fadd2_rn(a3, x[i + 3]);
+        }
+        a0 = __fadd2_rn(__fadd2_rn(a0, a1), __fadd2_rn(a2, a3));
+        const float mean = warp_sum(a0.x + a0.y) * inv_k;
+        a0 = a1 = a2 = a3 = make_float2(0.0f, 0.0f);
+        const float2 neg = make_float2(-mean, -mean);
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const bool valid = lane + 32 * j < units;
+#pragma unroll
+            for (int i = j * (VEC / 2); i < (j + 1) * (VEC / 2); i += 2) {
+                x[i] = valid ? __fadd2_rn(x[i], neg) : make_float2(0.0f, 0.0f);
+                x[i + 1] = valid ? __fadd2_rn(x[i + 1], neg) : make_float2(0.0f, 0.0f);
+                a0 = __ffma2_rn(x[i], x[i], a0);
+                a1 = __ffma2_rn(x[i + 1], x[i + 1], a1);
+            }
+        }
+        a0 = __fadd2_rn(a0, a1);
+        const float rstd = rsqrtf(fmaf(warp_sum(a0.x + a0.y), inv_k, p.eps));
+        if (p.mean != nullptr && lane == 0) {
+            p.mean[r] = mean;
+            p.rstd[r] = rstd;
+        }
+        const float2 rs = make_float2(rstd, rstd);
+        float m0 = 0.0f, m1 = 0.0f;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int u = lane + 32 * j;
+#pragma unroll
+            for (int q = 0; q < VEC / 4; ++q) {
+                const int i = j * (VEC / 2) + 2 * q;
+                float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b = w;
+                if (u < units) {
+                    w = sw[u * (VEC / 4) + q];
+                    b = sb[u * (VEC / 4) + q];
+                }
+                x[i] = __ffma2_rn(__fmul2_rn(x[i], rs), make_float2(w.x, w.y), make_float2(b.x, b.y));
+                x[i + 1] = __ffma2_rn(__fmul2_rn(x[i + 1], rs), make_float2(w.z, w.w), make_float2(b.z, b.w));
+                if constexpr (kQuant) {
+                    m0 = max3_abs(m0, x[i].x, x[i].y);
+                    m1 = max3_abs(m1, x[i + 1].x, x[i + 1].y);
+                }
+            }
+        }
+        if constexpr (!kQuant) {
+            T* out = static_cast<T*>(p.y) + r * p.K;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                float v[VEC];
+#pragma unroll
+                for (int i = 0; i < VEC / 2; ++i) {
+                    v[2 * i] = x[j * (VEC / 2) + i].x;
+                    v[2 * i + 1] = x[j * (VEC / 2) + i].y;
+                }
+                if (lane + 32 * j < units) Unit<T, VEC>::store(out, lane + 32 * j, v);
+            }
+        } else {
+            // non-negative floats compare as their bits do
+            const uint32_t bits = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fmaxf(m0, m1)));
+            const float sc = __fdiv_rn(fmaxf(__uint_as_float(bits), 1e-12f), p.qmax);
+            if (lane == 0) p.s[r] = sc;
+            float rcp;  // 1 ulp; with the product's half the quotient is good to 1.5
+            asm("rcp.approx.f32 %0, %1;" : "=f"(rcp) : "f"(sc));
+            const float2 rc = make_float2(rcp, rcp);
+            uint8_t* out = p.q + r * p.K;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                uint32_t c[VEC / 4];
+#pragma unroll
+                for (int q = 0; q < VEC / 4; ++q) {
+                    const int i = j * (VEC / 2) + 2 * q;
+                    c[q] = cvt_e4m3x4(__fmul2_rn(x[i], rc), __fmul2_rn(x[i + 1], rc));
+                }
+                const int u = lane + 32 * j;
+                if (u < units) {
+                    if constexpr (VEC == 8) reinterpret_cast<uint2*>(out)[u] = make_uint2(c[0], c[1]);
+                    else reinterpret_cast<uint32_t*>(out)[u] = c[0];
+                }
+            }
+        }
+        if (++slot == kWarpSlots) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
+}
+
 // ------------------------------------------------- launch shapes
 struct NormShape {
     bool vec;   // 16-byte units
@@ -1015,8 +1190,24 @@ RingKernel ring_backward(bool small) {
     return small ? norm_backward_ring_kernel<T, kRingSmall> : norm_backward_ring_kernel<T, kRingLarge>;
 }
 
-// Opt-in shared memory of the ring kernels (once per device).
+using WarpKernel = void (*)(const NormArgs, uint32_t*);
+
+// Columns per lane of the warp-per-row kernels: 32, 48, 64, 96, 128 or 160.
+template <typename T, bool kQuant>
+WarpKernel warp_kernel(int64_t K) {
+    if (K <= 32 * 32) return norm_warp_kernel<T, kQuant, 32>;
+    if (K <= 32 * 48) return norm_warp_kernel<T, kQuant, 48>;
+    if (K <= 32 * 64) return norm_warp_kernel<T, kQuant, 64>;
+    if (K <= 32 * 96) return norm_warp_kernel<T, kQuant, 96>;
+    if (K <= 32 * 128) return norm_warp_kernel<T, kQuant, 128>;
+    return norm_warp_kernel<T, kQuant, 160>;
+}
+
+size_t warp_smem(int64_t K, int elem) { return static_cast<size_t>(K) * (8 + kWarpRows * kWarpSlots * elem); }
+
+// Opt-in shared memory of the kernels with row slots (once per device).
 constexpr int kRingSmem = 160 * 1024;
+constexpr int kWarpSmem = 226 * 1024;
 template <typename T>
 cudaError_t ring_attributes_of() {
     cudaError_t e = cudaSuccess;
@@ -1026,6 +1217,9 @@ cudaError_t ring_attributes_of() {
         for (RingKernel f : k)
             if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
     }
+    for (int64_t columns : {32, 48, 64, 96, 128, 160})
+        for (WarpKernel f : {warp_kernel<T, false>(32 * columns), warp_kernel<T, true>(32 * columns)})
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kWarpSmem);
     return e;
 }
 tfq_status ring_attributes(DeviceState* ds) {
@@ -1087,6 +1281,23 @@ tfq_status launch_layer_norm(const NormCall& c, void* y, uint8_t* q, float* s, f
     a.qmax = qmax;
     a.clamp = q != nullptr && !is_e4m3_value(qmax);
     const RingShape ring = ring_shape(c.K, e, sh.vec, 1);
+    // One warp per row where every group has rows for a few CTAs of eight warps
+    // on every SM (fewer rows finish sooner with a CTA each: 8 x 5120 to codes
+    // 6.2 us against 8.1); a qmax that needs a clamp goes with the ring.
+    if (ring.threads > 0 && c.K <= 32 * 160 && warp_smem(c.K, e) <= kWarpSmem && a.clamp == 0 &&
+        c.M >= 2 * kWarpRows * ds->sm_count && c.M / c.groups >= 4 * kWarpRows) {
+        WarpKernel wk;
+        if (c.dtype == TFQ_DTYPE_FP32) wk = q ? warp_kernel<float, true>(c.K) : warp_kernel<float, false>(c.K);
+        else if (c.dtype == TFQ_DTYPE_FP16) wk = q ? warp_kernel<__half, true>(c.K) : warp_kernel<__half, false>(c.K);
+        else wk = q ? warp_kernel<__nv_bfloat16, true>(c.K) : warp_kernel<__nv_bfloat16, false>(c.K);
+        const tfq_status st = ring_attributes(ds);
+        if (st != TFQ_OK) return st;
+        const size_t smem = warp_smem(c.K, e);
+        const int64_t ctas = static_cast<int64_t>(ds->sm_count) * (c.K <= 32 * 64 && 2 * smem <= kWarpSmem ? 2 : 1);
+        a.parts = static_cast<int>(std::max<int64_t>(1, std::min(ctas / c.groups, c.M / c.groups / kWarpRows)));
+        return launch_error("layer norm", launch_kernel(wk, dim3(static_cast<unsigned>(a.parts * c.groups)),
+                                                        dim3(32 * kWarpRows), smem, stream, a, ds->err_word));
+    }
     if (ring.threads > 0) {
         const bool small = ring.threads <= kRingSmall;
         RingKernel rk;

@@ -80,7 +80,8 @@ def guard(shape, dtype, fill=77.0):
 
 SHAPES = [(1, 1), (1, 16), (3, 8), (5, 7), (33, 64), (300, 128), (7, 130), (64, 512), (2, 1001), (130, 1024),
           (9, 1536), (6, 2048), (5, 5120), (3, 8192), (3, 8200), (2, 12288), (2, 13824), (1, 32768), (2, 32767),
-          (1200, 96), (700, 520), (33, 640), (2, 10240), (2, 10256), (400, 1040), (1300, 5120)]
+          (1200, 96), (700, 520), (33, 640), (2, 10240), (2, 10256), (400, 1040), (1300, 5120),
+          (2400, 5120), (2500, 1536), (2401, 520), (2400, 2568), (2400, 4000), (2400, 1992)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
@@ -103,7 +104,8 @@ def test_forward(M, K, dtype):
     tfq.tfq_device_error()
 
 
-@pytest.mark.parametrize("M,K,G", [(12, 64, 3), (40, 1001, 5), (64, 5120, 4), (6, 96, 6), (600, 256, 2), (2000, 128, 2)])
+@pytest.mark.parametrize("M,K,G", [(12, 64, 3), (40, 1001, 5), (64, 5120, 4), (6, 96, 6), (600, 256, 2), (2000, 128, 2),
+                                   (7200, 1536, 3)])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_groups_equal_separate_calls(M, K, G, dtype):
     x, g = states(M, K, DT[dtype], 0, K)
@@ -132,7 +134,9 @@ def e4m3_spacing(v):
 @pytest.mark.parametrize("M,K,dtype", [(1, 16, "bf16"), (37, 64, "fp16"), (9, 144, "fp32"), (70, 1024, "bf16"),
                                        (5, 5120, "bf16"), (4, 5120, "fp32"), (3, 13824, "bf16"), (2, 32768, "bf16"),
                                        (2, 32768, "fp32"), (600, 256, "bf16"), (700, 528, "fp16"),
-                                       (33, 640, "fp32"), (2, 10240, "fp32"), (1300, 5120, "bf16")])
+                                       (33, 640, "fp32"), (2, 10240, "fp32"), (1300, 5120, "bf16"),
+                                       (2400, 5120, "fp16"), (2500, 1536, "bf16"), (2401, 528, "fp32"),
+                                       (2400, 2576, "bf16"), (2400, 4000, "bf16"), (2400, 2000, "fp32")])
 def test_quant(M, K, dtype, qmax):
     seed = M + K
     pad = (0, 3, 8)[seed % 3]
