@@ -543,8 +543,11 @@ __global__ void __launch_bounds__(256) norm_partials_kernel(const float* part_dw
     void* dst = blockIdx.y == 0 ? dw : db;
     if (part == nullptr) return;
     float s = 0.0f;
-    if (c < K)
-        for (int i = warp; i < parts; i += 8) s += part[(g * parts + i) * K + c];
+    if (c < K) {
+        const float* at = part + g * parts * K + c;
+#pragma unroll 8
+        for (int i = warp; i < parts; i += 8) s += at[static_cast<int64_t>(i) * K];
+    }
     sums[warp][lane] = s;
     __syncthreads();
     if (warp == 0 && c < K) {
@@ -925,17 +928,17 @@ __global__ void __launch_bounds__(kMaxThreads, kMaxThreads <= kRingSmall ? 2 : 1
     }
 }
 
-// ------------------------------------------------- one warp per row
-// Many wide rows (16-byte units, K up to 32 * 160): a warp holds a whole row as
-// fp32 pairs, C columns a lane, so that all three reductions are shuffles, no
-// barrier holds a row up and a row costs about 1000 instructions; the weight
-// (with its offset) and bias lie in shared memory as fp32, which every warp of
-// the CTA reads.  Each warp has two row slots of its own and the copy of its
-// row after next in flight.  A CTA stays within one group.  (Measured on B200,
-// 75600 x 5120 to codes: the CTA-per-row ring above 394 us, bound by
-// instructions and barriers.)
-constexpr int kWarpRows = 8;   // warps per CTA
-constexpr int kWarpSlots = 2;
+// ------------------------------------------------- one or two warps per row
+// Many wide rows (16-byte units, K up to 64 * 80): a row is held as fp32 pairs by
+// W warps (1 or 2), C columns a lane, so that the sums are shuffles and at most
+// one barrier of two warps joins them; a row costs some 1500 instructions of a
+// warp (those of the ring above 4000).  The weight (with its offset) and bias
+// lie in shared memory as fp32, which every row of the CTA reads.  Each row's
+// warps have one or two row slots of their own and copy the next rows into
+// them while they work on the present one.  A CTA stays within one group.
+// (Measured on B200, 75600 x 5120 to codes: the ring 394 us; W = 1, C = 160,
+// with spills, 270 us.)
+constexpr int kRowWarps = 16;  // warps per CTA, one CTA per SM
 
 __device__ __forceinline__ float max3_abs(float a, float b, float c) {
     float d;
@@ -943,36 +946,41 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
     return d;
 }
 
-template <typename T, bool kQuant, int C>
-__global__ void __launch_bounds__(32 * kWarpRows, C <= 64 ? 2 : 1) norm_warp_kernel(const NormArgs p, uint32_t* err) {
-    constexpr int VEC = 16 / sizeof(T), J = C / VEC, P = C / 2;
+template <typename T, bool kQuant, int C, int W>
+__global__ void __launch_bounds__(32 * kRowWarps, 1) norm_rows_kernel(const NormArgs p, int slots, uint32_t* err) {
+    constexpr int VEC = 16 / sizeof(T), J = C / VEC, P = C / 2, R = kRowWarps / W;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint64_t full[kWarpRows][kWarpSlots];
-    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    __shared__ uint64_t full[R][2];
+    __shared__ float joined[2][R][W][2];
+    __shared__ uint32_t joined_max[R][W];
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int row = warp / W, sub = warp % W, place = sub * 32 + lane;  // of the CTA's rows; of the row's threads
     const int units = p.K / VEC;
     const uint32_t row_bytes = static_cast<uint32_t>(p.K * sizeof(T));
-    float4* sw = reinterpret_cast<float4*>(smem);  // [K] weight + offset, then [K] bias
+    // weight + offset, then bias, each quad q of a 16-byte unit in a plane of its
+    // own, so that a warp's accesses are consecutive
+    float4* sw = reinterpret_cast<float4*>(smem);
     float4* sb = sw + p.K / 4;
-    uint8_t* ring = smem + 8 * static_cast<size_t>(p.K) + static_cast<size_t>(warp) * kWarpSlots * row_bytes;
-    if (lane == 0) {
-        for (int i = 0; i < kWarpSlots; ++i) mbar_init(&full[warp][i], 1);
+    uint8_t* ring = smem + 8 * static_cast<size_t>(p.K) + static_cast<size_t>(row * slots) * row_bytes;
+    if (place == 0) {
+        mbar_init(&full[row][0], 1);
+        mbar_init(&full[row][1], 1);
         fence_mbar_init();
     }
     pdl_allow_next();
     pdl_wait();
     const int64_t g = blockIdx.x / static_cast<unsigned>(p.parts);
     const int64_t part = blockIdx.x % static_cast<unsigned>(p.parts);
-    // the group's rows, dealt to its parts * kWarpRows warps in turn
-    const int64_t first = g * p.group_rows + part * kWarpRows + warp, last = (g + 1) * p.group_rows;
-    const int64_t step = static_cast<int64_t>(p.parts) * kWarpRows;
-    __syncwarp();
+    // the group's rows, dealt to its parts * R rows at a time in turn
+    const int64_t first = g * p.group_rows + part * R + row, last = (g + 1) * p.group_rows;
+    const int64_t step = static_cast<int64_t>(p.parts) * R;
     const auto fetch = [&](int64_t r, int slot) {
-        mbar_arrive_expect_tx(&full[warp][slot], row_bytes);
-        bulk_g2s(ring + slot * row_bytes, static_cast<const T*>(p.x) + r * p.x_stride, row_bytes, &full[warp][slot]);
+        mbar_arrive_expect_tx(&full[row][slot], row_bytes);
+        bulk_g2s(ring + slot * row_bytes, static_cast<const T*>(p.x) + r * p.x_stride, row_bytes, &full[row][slot]);
     };
-    if (lane == 0)
-        for (int i = 0; i < kWarpSlots && first + i * step < last; ++i) fetch(first + i * step, i);
-    for (int c = t; c < p.K; c += 32 * kWarpRows) {
+    if (place == 0)
+        for (int i = 0; i < slots && first + i * step < last; ++i) fetch(first + i * step, i);
+    for (int c = t; c < p.K; c += 32 * kRowWarps) {
         const int64_t at = g * p.K + c;
         float w[1] = {1.0f}, b[1] = {0.0f};
         if (p.w != nullptr) {
@@ -980,15 +988,30 @@ __global__ void __launch_bounds__(32 * kWarpRows, C <= 64 ? 2 : 1) norm_warp_ker
             w[0] += p.offset;
         }
         if (p.b != nullptr) load_affine<T, 1>(b, p.b, p.w_f32, at);
-        reinterpret_cast<float*>(sw)[c] = w[0];
-        reinterpret_cast<float*>(sb)[c] = b[0];
+        const int to = ((c % VEC / 4) * units + c / VEC) * 4 + c % 4;
+        reinterpret_cast<float*>(sw)[to] = w[0];
+        reinterpret_cast<float*>(sb)[to] = b[0];
     }
+    bool valid[J];
+    int mine = 0;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        valid[j] = place + 32 * W * j < units;
+        mine += valid[j] ? VEC : 0;
+    }
+    // columns of this warp and of the row's other one
+    const float n_warp = warp_sum(static_cast<float>(mine)), n_other = static_cast<float>(p.K) - n_warp;
+    const float inv_n_warp = n_warp > 0.0f ? 1.0f / n_warp : 0.0f, inv_n_other = n_other > 0.0f ? 1.0f / n_other : 0.0f;
     __syncthreads();
+    const auto row_sync = [&]() {
+        if constexpr (W == 1) __syncwarp();
+        else named_bar_sync(1 + row, 32 * W);
+    };
     const float inv_k = 1.0f / static_cast<float>(p.K);
-    int slot = 0;
+    int slot = 0, par = 0;
     uint32_t phase = 0;
-    for (int64_t r = first; r < last; r += step) {
-        if (!mbar_wait(&full[warp][slot], phase, nullptr)) {
+    for (int64_t r = first; r < last; r += step, par ^= 1) {
+        if (!mbar_wait(&full[row][slot], phase, nullptr)) {
             atomicOr(err, kErrNorm);
             break;
         }
@@ -996,61 +1019,76 @@ __global__ void __launch_bounds__(32 * kWarpRows, C <= 64 ? 2 : 1) norm_warp_ker
         const uint4* src = reinterpret_cast<const uint4*>(ring + slot * row_bytes);
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            const int u = lane + 32 * j;
             Unit<T, VEC> raw;
             raw.clear();
-            if (u < units) raw.raw = src[u];
+            if (valid[j]) raw.raw = src[place + 32 * W * j];
             float v[VEC];
             raw.get(v);
 #pragma unroll
             for (int i = 0; i < VEC / 2; ++i) x[j * (VEC / 2) + i] = make_float2(v[2 * i], v[2 * i + 1]);
         }
-        __syncwarp();
-        if (lane == 0 && r + kWarpSlots * step < last) fetch(r + kWarpSlots * step, slot);
-        float2 a0 = make_float2(0.0f, 0.0f), a1 = a0, a2 = a0, a3 = a0;
+        float2 a0 = x[0], a1 = x[1];
 #pragma unroll
-        for (int i = 0; i < P; i += 4) {
+        for (int i = 2; i < P; i += 2) {
             a0 = __fadd2_rn(a0, x[i]);
             a1 = __fadd2_rn(a1, x[i + 1]);
-            a2 = __fadd2_rn(a2, x[i + 2]);
-            a3 = __fadd2_rn(a3, x[i + 3]);
         }
-        a0 = __fadd2_rn(__fadd2_rn(a0, a1), __fadd2_rn(a2, a3));
-        const float mean = warp_sum(a0.x + a0.y) * inv_k;
-        a0 = a1 = a2 = a3 = make_float2(0.0f, 0.0f);
-        const float2 neg = make_float2(-mean, -mean);
+        a0 = __fadd2_rn(a0, a1);
+        const float sum_w = warp_sum(a0.x + a0.y);
+        const float mean_w = sum_w * inv_n_warp;
+        a0 = a1 = make_float2(0.0f, 0.0f);
+        const float2 neg_w = make_float2(-mean_w, -mean_w);
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            const bool valid = lane + 32 * j < units;
 #pragma unroll
             for (int i = j * (VEC / 2); i < (j + 1) * (VEC / 2); i += 2) {
-                x[i] = valid ? __fadd2_rn(x[i], neg) : make_float2(0.0f, 0.0f);
-                x[i + 1] = valid ? __fadd2_rn(x[i + 1], neg) : make_float2(0.0f, 0.0f);
-                a0 = __ffma2_rn(x[i], x[i], a0);
-                a1 = __ffma2_rn(x[i + 1], x[i + 1], a1);
+                const float2 d0 = __fadd2_rn(x[i], neg_w), d1 = __fadd2_rn(x[i + 1], neg_w);
+                if (valid[j]) {
+                    a0 = __ffma2_rn(d0, d0, a0);
+                    a1 = __ffma2_rn(d1, d1, a1);
+                }
             }
         }
         a0 = __fadd2_rn(a0, a1);
-        const float rstd = rsqrtf(fmaf(warp_sum(a0.x + a0.y), inv_k, p.eps));
-        if (p.mean != nullptr && lane == 0) {
+        float m2 = warp_sum(a0.x + a0.y), mean = mean_w;
+        if constexpr (W == 2) {
+            if (lane == 0) {
+                joined[par][row][sub][0] = sum_w;
+                joined[par][row][sub][1] = m2;
+            }
+            row_sync();
+            // both warps get the same bits: the terms are added in the warps' order
+            const float s0 = joined[par][row][0][0], s1 = joined[par][row][1][0];
+            mean = (s0 + s1) * inv_k;
+            const float n0 = sub == 0 ? n_warp : n_other, n1 = sub == 0 ? n_other : n_warp;
+            const float d0 = fmaf(s0, sub == 0 ? inv_n_warp : inv_n_other, -mean);
+            const float d1 = fmaf(s1, sub == 0 ? inv_n_other : inv_n_warp, -mean);
+            m2 = fmaf(n0 * d0, d0, joined[par][row][0][1]) + fmaf(n1 * d1, d1, joined[par][row][1][1]);
+        } else {
+            row_sync();
+        }
+        // every lane has its columns: the slot takes the row `slots` steps on
+        if (place == 0 && r + slots * step < last) fetch(r + slots * step, slot);
+        const float rstd = rsqrtf(fmaf(m2, inv_k, p.eps));
+        if (p.mean != nullptr && place == 0) {
             p.mean[r] = mean;
             p.rstd[r] = rstd;
         }
-        const float2 rs = make_float2(rstd, rstd);
+        const float2 rs = make_float2(rstd, rstd), neg = make_float2(-mean, -mean);
         float m0 = 0.0f, m1 = 0.0f;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            const int u = lane + 32 * j;
 #pragma unroll
             for (int q = 0; q < VEC / 4; ++q) {
-                const int i = j * (VEC / 2) + 2 * q;
+                const int i = j * (VEC / 2) + 2 * q, at = q * units + place + 32 * W * j;
                 float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b = w;
-                if (u < units) {
-                    w = sw[u * (VEC / 4) + q];
-                    b = sb[u * (VEC / 4) + q];
+                if (valid[j]) {
+                    w = sw[at];
+                    b = sb[at];
                 }
-                x[i] = __ffma2_rn(__fmul2_rn(x[i], rs), make_float2(w.x, w.y), make_float2(b.x, b.y));
-                x[i + 1] = __ffma2_rn(__fmul2_rn(x[i + 1], rs), make_float2(w.z, w.w), make_float2(b.z, b.w));
+                x[i] = __ffma2_rn(__fmul2_rn(__fadd2_rn(x[i], neg), rs), make_float2(w.x, w.y), make_float2(b.x, b.y));
+                x[i + 1] = __ffma2_rn(__fmul2_rn(__fadd2_rn(x[i + 1], neg), rs), make_float2(w.z, w.w),
+                                      make_float2(b.z, b.w));
                 if constexpr (kQuant) {
                     m0 = max3_abs(m0, x[i].x, x[i].y);
                     m1 = max3_abs(m1, x[i + 1].x, x[i + 1].y);
@@ -1067,13 +1105,18 @@ __global__ void __launch_bounds__(32 * kWarpRows, C <= 64 ? 2 : 1) norm_warp_ker
                     v[2 * i] = x[j * (VEC / 2) + i].x;
                     v[2 * i + 1] = x[j * (VEC / 2) + i].y;
                 }
-                if (lane + 32 * j < units) Unit<T, VEC>::store(out, lane + 32 * j, v);
+                if (valid[j]) Unit<T, VEC>::store(out, place + 32 * W * j, v);
             }
         } else {
             // non-negative floats compare as their bits do
-            const uint32_t bits = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fmaxf(m0, m1)));
+            uint32_t bits = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fmaxf(m0, m1)));
+            if constexpr (W == 2) {
+                if (lane == 0) joined_max[row][sub] = bits;
+                row_sync();
+                bits = max(joined_max[row][0], joined_max[row][1]);
+            }
             const float sc = __fdiv_rn(fmaxf(__uint_as_float(bits), 1e-12f), p.qmax);
-            if (lane == 0) p.s[r] = sc;
+            if (place == 0) p.s[r] = sc;
             float rcp;  // 1 ulp; with the product's half the quotient is good to 1.5
             asm("rcp.approx.f32 %0, %1;" : "=f"(rcp) : "f"(sc));
             const float2 rc = make_float2(rcp, rcp);
@@ -1086,14 +1129,14 @@ __global__ void __launch_bounds__(32 * kWarpRows, C <= 64 ? 2 : 1) norm_warp_ker
                     const int i = j * (VEC / 2) + 2 * q;
                     c[q] = cvt_e4m3x4(__fmul2_rn(x[i], rc), __fmul2_rn(x[i + 1], rc));
                 }
-                const int u = lane + 32 * j;
-                if (u < units) {
+                const int u = place + 32 * W * j;
+                if (valid[j]) {
                     if constexpr (VEC == 8) reinterpret_cast<uint2*>(out)[u] = make_uint2(c[0], c[1]);
                     else reinterpret_cast<uint32_t*>(out)[u] = c[0];
                 }
             }
         }
-        if (++slot == kWarpSlots) {
+        if (++slot == slots) {
             slot = 0;
             phase ^= 1u;
         }
@@ -1146,8 +1189,8 @@ RingShape ring_shape(int64_t K, int elem, bool vec, int rows_per_slot) {
     if (!vec || threads <= 32 || threads > kRingLarge) return {0, 0, 0, 0};
     const int64_t slot = K * elem * rows_per_slot;
     const int per_sm = std::min(8, std::max(1, 21 / (threads / 32)));  // at 96 registers 21 warps fit
-    // about 96 KB of rows in flight per SM
-    const int slots = static_cast<int>(std::max<int64_t>(2, std::min<int64_t>(kRingMaxSlots, 96 * 1024 / (slot * per_sm))));
+    // about 144 KB of rows in flight per SM
+    const int slots = static_cast<int>(std::max<int64_t>(2, std::min<int64_t>(kRingMaxSlots, 144 * 1024 / (slot * per_sm))));
     return {threads, per_sm, slots, static_cast<size_t>(slot * slots)};
 }
 
@@ -1190,24 +1233,35 @@ RingKernel ring_backward(bool small) {
     return small ? norm_backward_ring_kernel<T, kRingSmall> : norm_backward_ring_kernel<T, kRingLarge>;
 }
 
-using WarpKernel = void (*)(const NormArgs, uint32_t*);
+// The kernels of one or two warps per row: up to 80 columns a lane.
+struct RowsShape {
+    RingKernel kernel;  // null: not for these rows
+    int rows;           // rows per CTA at a time
+    int slots;
+    size_t smem;
+};
+constexpr int kRingSmem = 160 * 1024;
+constexpr int kRowsSmem = 226 * 1024;
+constexpr int kRowsMaxK = 64 * 80;
 
-// Columns per lane of the warp-per-row kernels: 32, 48, 64, 96, 128 or 160.
 template <typename T, bool kQuant>
-WarpKernel warp_kernel(int64_t K) {
-    if (K <= 32 * 32) return norm_warp_kernel<T, kQuant, 32>;
-    if (K <= 32 * 48) return norm_warp_kernel<T, kQuant, 48>;
-    if (K <= 32 * 64) return norm_warp_kernel<T, kQuant, 64>;
-    if (K <= 32 * 96) return norm_warp_kernel<T, kQuant, 96>;
-    if (K <= 32 * 128) return norm_warp_kernel<T, kQuant, 128>;
-    return norm_warp_kernel<T, kQuant, 160>;
+RowsShape rows_shape(int64_t K) {
+    RowsShape s = {nullptr, K <= 32 * 80 ? kRowWarps : kRowWarps / 2, 2, 0};
+    const int64_t row = K * sizeof(T);
+    if (8 * K + s.rows * 2 * row > kRowsSmem) s.slots = 1;
+    s.smem = static_cast<size_t>(8 * K + s.rows * s.slots * row);
+    if (s.smem > kRowsSmem || K > kRowsMaxK) return s;
+    s.kernel = K <= 32 * 32   ? norm_rows_kernel<T, kQuant, 32, 1>
+               : K <= 32 * 48 ? norm_rows_kernel<T, kQuant, 48, 1>
+               : K <= 32 * 64 ? norm_rows_kernel<T, kQuant, 64, 1>
+               : K <= 32 * 80 ? norm_rows_kernel<T, kQuant, 80, 1>
+               : K <= 64 * 48 ? norm_rows_kernel<T, kQuant, 48, 2>
+               : K <= 64 * 64 ? norm_rows_kernel<T, kQuant, 64, 2>
+                              : norm_rows_kernel<T, kQuant, 80, 2>;
+    return s;
 }
 
-size_t warp_smem(int64_t K, int elem) { return static_cast<size_t>(K) * (8 + kWarpRows * kWarpSlots * elem); }
-
 // Opt-in shared memory of the kernels with row slots (once per device).
-constexpr int kRingSmem = 160 * 1024;
-constexpr int kWarpSmem = 226 * 1024;
 template <typename T>
 cudaError_t ring_attributes_of() {
     cudaError_t e = cudaSuccess;
@@ -1217,9 +1271,12 @@ cudaError_t ring_attributes_of() {
         for (RingKernel f : k)
             if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
     }
-    for (int64_t columns : {32, 48, 64, 96, 128, 160})
-        for (WarpKernel f : {warp_kernel<T, false>(32 * columns), warp_kernel<T, true>(32 * columns)})
-            if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kWarpSmem);
+    for (int K : {32 * 32, 32 * 48, 32 * 64, 32 * 80, 64 * 48, 64 * 64, 64 * 80}) {
+        const RingKernel k[2] = {rows_shape<T, false>(K).kernel, rows_shape<T, true>(K).kernel};
+        for (RingKernel f : k)
+            if (e == cudaSuccess && f != nullptr)
+                e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowsSmem);
+    }
     return e;
 }
 tfq_status ring_attributes(DeviceState* ds) {
@@ -1281,22 +1338,24 @@ tfq_status launch_layer_norm(const NormCall& c, void* y, uint8_t* q, float* s, f
     a.qmax = qmax;
     a.clamp = q != nullptr && !is_e4m3_value(qmax);
     const RingShape ring = ring_shape(c.K, e, sh.vec, 1);
-    // One warp per row where every group has rows for a few CTAs of eight warps
-    // on every SM (fewer rows finish sooner with a CTA each: 8 x 5120 to codes
-    // 6.2 us against 8.1); a qmax that needs a clamp goes with the ring.
-    if (ring.threads > 0 && c.K <= 32 * 160 && warp_smem(c.K, e) <= kWarpSmem && a.clamp == 0 &&
-        c.M >= 2 * kWarpRows * ds->sm_count && c.M / c.groups >= 4 * kWarpRows) {
-        WarpKernel wk;
-        if (c.dtype == TFQ_DTYPE_FP32) wk = q ? warp_kernel<float, true>(c.K) : warp_kernel<float, false>(c.K);
-        else if (c.dtype == TFQ_DTYPE_FP16) wk = q ? warp_kernel<__half, true>(c.K) : warp_kernel<__half, false>(c.K);
-        else wk = q ? warp_kernel<__nv_bfloat16, true>(c.K) : warp_kernel<__nv_bfloat16, false>(c.K);
-        const tfq_status st = ring_attributes(ds);
-        if (st != TFQ_OK) return st;
-        const size_t smem = warp_smem(c.K, e);
-        const int64_t ctas = static_cast<int64_t>(ds->sm_count) * (c.K <= 32 * 64 && 2 * smem <= kWarpSmem ? 2 : 1);
-        a.parts = static_cast<int>(std::max<int64_t>(1, std::min(ctas / c.groups, c.M / c.groups / kWarpRows)));
-        return launch_error("layer norm", launch_kernel(wk, dim3(static_cast<unsigned>(a.parts * c.groups)),
-                                                        dim3(32 * kWarpRows), smem, stream, a, ds->err_word));
+    // One or two warps per row where every SM has rows for all of its warps twice
+    // over, and every group some too (fewer rows finish sooner with a CTA each:
+    // 8 x 5120 to codes 6.2 us against 8.1); a qmax that needs a clamp goes
+    // with the ring.
+    if (ring.threads > 0 && a.clamp == 0 && c.M >= 2 * kRowWarps * ds->sm_count && c.M / c.groups >= 4 * kRowWarps) {
+        RowsShape rows;
+        if (c.dtype == TFQ_DTYPE_FP32) rows = q ? rows_shape<float, true>(c.K) : rows_shape<float, false>(c.K);
+        else if (c.dtype == TFQ_DTYPE_FP16) rows = q ? rows_shape<__half, true>(c.K) : rows_shape<__half, false>(c.K);
+        else rows = q ? rows_shape<__nv_bfloat16, true>(c.K) : rows_shape<__nv_bfloat16, false>(c.K);
+        if (rows.kernel != nullptr) {
+            const tfq_status st = ring_attributes(ds);
+            if (st != TFQ_OK) return st;
+            a.parts = static_cast<int>(std::max<int64_t>(
+                1, std::min<int64_t>(ds->sm_count / c.groups, c.M / c.groups / rows.rows)));
+            return launch_error("layer norm", launch_kernel(rows.kernel, dim3(static_cast<unsigned>(a.parts * c.groups)),
+                                                            dim3(32 * kRowWarps), rows.smem, stream, a, rows.slots,
+                                                            ds->err_word));
+        }
     }
     if (ring.threads > 0) {
         const bool small = ring.threads <= kRingSmall;

@@ -81,7 +81,7 @@ def guard(shape, dtype, fill=77.0):
 SHAPES = [(1, 1), (1, 16), (3, 8), (5, 7), (33, 64), (300, 128), (7, 130), (64, 512), (2, 1001), (130, 1024),
           (9, 1536), (6, 2048), (5, 5120), (3, 8192), (3, 8200), (2, 12288), (2, 13824), (1, 32768), (2, 32767),
           (1200, 96), (700, 520), (33, 640), (2, 10240), (2, 10256), (400, 1040), (1300, 5120),
-          (2400, 5120), (2500, 1536), (2401, 520), (2400, 2568), (2400, 4000), (2400, 1992)]
+          (4800, 5120), (4900, 1536), (4801, 520), (4800, 2568), (4800, 4000), (4800, 1992), (4800, 2504)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
@@ -105,7 +105,7 @@ def test_forward(M, K, dtype):
 
 
 @pytest.mark.parametrize("M,K,G", [(12, 64, 3), (40, 1001, 5), (64, 5120, 4), (6, 96, 6), (600, 256, 2), (2000, 128, 2),
-                                   (7200, 1536, 3)])
+                                   (15000, 1536, 3)])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_groups_equal_separate_calls(M, K, G, dtype):
     x, g = states(M, K, DT[dtype], 0, K)
@@ -115,7 +115,7 @@ def test_groups_equal_separate_calls(M, K, G, dtype):
     n = M // G
     for i in range(G):
         rows = slice(i * n, (i + 1) * n)
-        # a group's rows start wherever they start: the same kernel, or the element form, whose sums run in another order
+        # few rows or many in both calls: the same kernel and the same order of sums
         part = tfq.tfq_layer_norm(x[rows].contiguous(), w[i].contiguous(), b[i].contiguous(), weight_offset=1.0)
         assert torch.equal(part, y[rows])
         if q is not None:
@@ -135,8 +135,9 @@ def e4m3_spacing(v):
                                        (5, 5120, "bf16"), (4, 5120, "fp32"), (3, 13824, "bf16"), (2, 32768, "bf16"),
                                        (2, 32768, "fp32"), (600, 256, "bf16"), (700, 528, "fp16"),
                                        (33, 640, "fp32"), (2, 10240, "fp32"), (1300, 5120, "bf16"),
-                                       (2400, 5120, "fp16"), (2500, 1536, "bf16"), (2401, 528, "fp32"),
-                                       (2400, 2576, "bf16"), (2400, 4000, "bf16"), (2400, 2000, "fp32")])
+                                       (4800, 5120, "fp16"), (4900, 1536, "bf16"), (4801, 528, "fp32"),
+                                       (4800, 2576, "bf16"), (4800, 4000, "bf16"), (4800, 2000, "fp32"),
+                                       (4800, 2512, "bf16")])
 def test_quant(M, K, dtype, qmax):
     seed = M + K
     pad = (0, 3, 8)[seed % 3]
