@@ -56,6 +56,7 @@ def _streamed(fn):
 
 
 def _operand(t, name, dtype=None, ndim=None, device=None):
+    """Refuses what is not a CUDA tensor of this type, dimension and device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -69,13 +70,14 @@ def _operand(t, name, dtype=None, ndim=None, device=None):
 
 
 def _dense(t, name, dtype, shape, device):
-    """A contiguous operand of exactly this type and shape."""
+    """A contiguous operand of exactly this type and shape (a tuple)."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device
+            and t.is_contiguous()):
+        return t  # the usual case, in as few steps as it takes: small calls are bound by them
     _operand(t, name, dtype, None, device)
-    if t.shape != torch.Size(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _codes(t, name, device):
@@ -87,24 +89,44 @@ def _codes(t, name, device):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _output(t, name, dtype, shape, device):
+def _output(t, name, dtype, shape, like):
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=f"cuda:{device}")
-    return _dense(t, name, dtype, shape, device)
+        return like.new_empty(shape, dtype=dtype)
+    return _dense(t, name, dtype, shape, like.get_device())
+
+
+def _workspace(t, need, like):
+    if t is None:
+        return like.new_empty((need,), dtype=torch.uint8)
+    _operand(t, "workspace", torch.uint8, 1, like.get_device())
+    if t.numel() < need or not t.is_contiguous():
+        raise ValueError(f"workspace must hold {need} contiguous bytes")
+    return t
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+_functions = {}
+_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
+def _function(name):
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(load_library(), name)
+    return fn
+
+
 def _call(name, device, *args):
     """Calls the C entry point on `device`'s current stream."""
-    fn = getattr(load_library(), name)
-    if device == torch.cuda.current_device():
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(device))
+    fn = _functions.get(name) or _function(name)
+    if device == _current_device():
+        st = fn(*args, _raw_stream(device))
     else:
         with torch.cuda.device(device):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(device))
+            st = fn(*args, _raw_stream(device))
     if st:
         _check(st, name)
 
@@ -113,13 +135,14 @@ def _rows(t, name, dtype=None, device=None):
     """(row stride) of a matrix whose rows are contiguous."""
     _operand(t, name, dtype, 2, device)
     M, K = t.shape
-    if K > 1 and t.stride(1) != 1:
+    row, element = t.stride()
+    if K > 1 and element != 1:
         raise ValueError(f"{name} must have contiguous rows")
     if M <= 1:
         return K
-    if t.stride(0) < K:
+    if row < K:
         raise ValueError(f"{name} must not have overlapping rows")
-    return t.stride(0)
+    return row
 
 
 def _affine(weight, bias, x, K, device):
@@ -159,10 +182,10 @@ def tfq_layer_norm(x, weight=None, bias=None, eps: float = 1e-6, weight_offset: 
     dev = x.get_device()
     M, K = x.shape
     groups, wdt = _affine(weight, bias, x, K, dev)
-    y = _output(y, "y", x.dtype, (M, K), dev)
+    y = _output(y, "y", x.dtype, (M, K), x)
     mean = rstd = None
     if stats:
-        mean, rstd = torch.empty((2, M), dtype=torch.float32, device=x.device).unbind(0)
+        mean, rstd = x.new_empty((2, M), dtype=torch.float32).unbind(0)
     _call("tfq_layer_norm", dev, x.data_ptr(), stride, dtype, _ptr(weight), _ptr(bias), _DTYPES[wdt], weight_offset,
           M, K, groups, eps, y.data_ptr(), _ptr(mean), _ptr(rstd))
     return (y, mean, rstd) if stats else y
@@ -178,8 +201,8 @@ def tfq_layer_norm_quant_fp8(x, weight=None, bias=None, eps: float = 1e-6, weigh
     dev = x.get_device()
     M, K = x.shape
     groups, wdt = _affine(weight, bias, x, K, dev)
-    q = _output(q, "q", torch.uint8, (M, K), dev)
-    s = _output(s, "s", torch.float32, (M,), dev)
+    q = _output(q, "q", torch.uint8, (M, K), x)
+    s = _output(s, "s", torch.float32, (M,), x)
     _call("tfq_layer_norm_quant_fp8", dev, x.data_ptr(), stride, dtype, _ptr(weight), _ptr(bias), _DTYPES[wdt],
           weight_offset, M, K, groups, eps, qmax, q.data_ptr(), s.data_ptr())
     return q, s
@@ -187,7 +210,7 @@ def tfq_layer_norm_quant_fp8(x, weight=None, bias=None, eps: float = 1e-6, weigh
 
 def tfq_layer_norm_backward_workspace_bytes(M: int, K: int, groups: int = 1) -> int:
     """Bytes of the workspace tfq_layer_norm_backward needs for weight or bias gradients."""
-    return int(load_library().tfq_layer_norm_backward_workspace_bytes(int(M), int(K), int(groups)))
+    return _function("tfq_layer_norm_backward_workspace_bytes")(int(M), int(K), int(groups))
 
 
 @_streamed
@@ -223,16 +246,11 @@ def tfq_layer_norm_backward(dy, x, weight, mean, rstd, weight_offset: float = 0.
         if groups < 1 or M % groups:
             raise ValueError(f"{M} rows do not make {groups} equal groups")
         need_weight = False
-    dx = torch.empty((M, K), dtype=x.dtype, device=x.device) if need_x else None
-    dw = torch.empty(shape, dtype=wdt, device=x.device) if need_weight else None
-    db = torch.empty(shape, dtype=wdt, device=x.device) if need_bias else None
+    dx = x.new_empty((M, K)) if need_x else None
+    dw = x.new_empty(shape, dtype=wdt) if need_weight else None
+    db = x.new_empty(shape, dtype=wdt) if need_bias else None
     if need_weight or need_bias:
-        n = tfq_layer_norm_backward_workspace_bytes(M, K, groups)
-        if workspace is None:
-            workspace = torch.empty((n,), dtype=torch.uint8, device=x.device)
-        _operand(workspace, "workspace", torch.uint8, 1, dev)
-        if workspace.numel() < n or not workspace.is_contiguous():
-            raise ValueError(f"workspace must hold {n} contiguous bytes")
+        workspace = _workspace(workspace, tfq_layer_norm_backward_workspace_bytes(M, K, groups), x)
     else:
         workspace = None
     _call("tfq_layer_norm_backward", dev, dy.data_ptr(), dy_stride, x.data_ptr(), x_stride, dtype, _ptr(weight),
@@ -270,7 +288,7 @@ def _heads(t, name, dtype, device, M, D):
 
 def _rope_output(out, name, like, device):
     if out is None:
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+        return like.new_empty(like.shape)
     _heads(out, name, like.dtype, device, like.shape[0], like.shape[2])
     if out.shape[1] != like.shape[1]:
         raise ValueError(f"{name} must have {like.shape[1]} heads")
@@ -343,14 +361,14 @@ def tfq_lora_fold(lora_B, scaling, s_w, out=None):
     if scaling is not None:
         _dense(scaling, "scaling", torch.float32, (n,), dev)
     _dense(s_w, "s_w", torch.float32, (N,), dev)
-    out = _output(out, "out", torch.bfloat16, (n, N, R), dev)
+    out = _output(out, "out", torch.bfloat16, (n, N, R), lora_B)
     _call("tfq_lora_fold", dev, lora_B.data_ptr(), _ptr(scaling), s_w.data_ptr(), n, N, R, out.data_ptr())
     return out
 
 
 def tfq_scaled_fp8_linear_lora_workspace_bytes(M: int, R: int) -> int:
     """Bytes of the workspace tfq_scaled_fp8_linear_lora needs for M rows and rank R."""
-    return int(load_library().tfq_scaled_fp8_linear_lora_workspace_bytes(int(M), int(R)))
+    return _function("tfq_scaled_fp8_linear_lora_workspace_bytes")(int(M), int(R))
 
 
 @_streamed
@@ -376,14 +394,8 @@ def tfq_scaled_fp8_linear_lora(A_q, s_a, W_q, s_w, x, lora_A, lora_Bs, adapter, 
     _dense(adapter, "adapter", torch.int32, (M,), dev)
     if bias is not None:
         _dense(bias, "bias", torch.bfloat16, (N,), dev)
-    out = _output(out, "out", torch.bfloat16, (M, N), dev)
-    need = tfq_scaled_fp8_linear_lora_workspace_bytes(M, R)
-    if workspace is None:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=A_q.device)
-    else:
-        _operand(workspace, "workspace", torch.uint8, 1, dev)
-        if workspace.numel() < need or not workspace.is_contiguous():
-            raise ValueError(f"workspace must hold {need} contiguous bytes")
+    out = _output(out, "out", torch.bfloat16, (M, N), x)
+    workspace = _workspace(workspace, tfq_scaled_fp8_linear_lora_workspace_bytes(M, R), x)
     _call("tfq_scaled_fp8_linear_lora", dev, A_q.data_ptr(), s_a.data_ptr(), W_q.data_ptr(), s_w.data_ptr(),
           _ptr(bias), M, N, K, x.data_ptr(), lora_A.data_ptr(), lora_Bs.data_ptr(), adapter.data_ptr(), n, R,
           out.data_ptr(), workspace.data_ptr())
