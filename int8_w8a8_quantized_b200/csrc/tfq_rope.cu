@@ -89,33 +89,23 @@ struct Chunk {  // VEC elements of T, moved as one 16-byte access (VEC > 1) or o
 
 // kHalves: an item is the VEC elements at i and their partners at P + i, else
 // VEC consecutive elements (VEC / 2 pairs), two single ones in the form
-// without alignment (VEC == 1).
+// without alignment (VEC == 1).  A thread has one place within a head and
+// walks (token, head) pairs, kBatch of them in flight; the first batch's loads
+// are issued before the table is formed.
 template <typename T, int VEC, bool kHalves>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs p) {
-    constexpr bool kTwo = kHalves || VEC == 1;         // an item is two chunks
-    constexpr int kPairs = kTwo ? VEC : VEC / 2;       // pairs per item
-    constexpr int kHeads = kTwo ? 2 : 4;               // heads in flight per thread
-    extern __shared__ float2 table[];                  // [tokens][pairs] (cos, sin)
+    constexpr bool kTwo = kHalves || VEC == 1;  // an item is two chunks
+    constexpr int kPairs = kTwo ? VEC : VEC / 2;
+    constexpr int kBatch = 4;
+    extern __shared__ float2 table[];           // [tokens][pairs] (cos, sin)
     pdl_allow_next();
     pdl_wait();
     const int64_t m0 = static_cast<int64_t>(blockIdx.x) * p.tokens;
     const int here = static_cast<int>(min(static_cast<int64_t>(p.tokens), p.M - m0));
-    for (int e = threadIdx.x; e < here * p.pairs; e += kRopeThreads) {
-        const int tok = e / p.pairs, i = e - tok * p.pairs;
-        const int64_t at = (m0 + tok) * p.pos_row_stride + p.axis[i] * p.pos_axis_stride;
-        const double pos = p.pos64 ? static_cast<double>(static_cast<const int64_t*>(p.pos)[at])
-                                   : static_cast<double>(static_cast<const int32_t*>(p.pos)[at]);
-        const double turns = pos * p.inv_turn[i];
-        float s, c;
-        sincospif(2.0f * static_cast<float>(turns - rint(turns)), &s, &c);
-        table[e] = make_float2(c, p.inverse ? -s : s);
-    }
-    __syncthreads();
     const int heads = p.q.heads + p.k.heads;
     const int per_token = p.items * p.head_lanes;
     const int slot = threadIdx.x / per_token;
     const int slots = kRopeThreads / per_token;
-    if (slot >= slots) return;
     const int in_token = threadIdx.x - slot * per_token;
     const int h0 = in_token / p.items;
     const int item = in_token - h0 * p.items;
@@ -133,60 +123,79 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     } else {
         o0 = o1 = item * VEC;
     }
-    for (int tok = slot; tok < here; tok += slots) {
-        float2 cs[kPairs];
-        if (rotates) {
+    Chunk<T, VEC> a[kBatch], b[kTwo ? kBatch : 1];
+    T* out[kBatch];
+    int tokens[kBatch];  // of the batch's items, -1: none
+    int tok = slot < slots ? slot : here, h = h0;  // the next (token, head)
+    const auto load = [&]() {
 #pragma unroll
-            for (int i = 0; i < kPairs; ++i) cs[i] = table[tok * p.pairs + item * kPairs + i];
-        }
-        const int64_t m = m0 + tok;
-        for (int hb = h0; hb < heads; hb += kHeads * p.head_lanes) {
-            Chunk<T, VEC> a[kHeads], b[kTwo ? kHeads : 1];
-            T* out[kHeads];
-#pragma unroll
-            for (int j = 0; j < kHeads; ++j) {
-                const int h = hb + j * p.head_lanes;
-                if (h < heads) {
-                    const bool is_k = h >= p.q.heads;
-                    const RopeTensor& t = is_k ? p.k : p.q;
-                    const int hl = is_k ? h - p.q.heads : h;
-                    const T* in = static_cast<const T*>(t.in) + m * t.row_stride + hl * t.head_stride;
-                    out[j] = static_cast<T*>(t.out) + m * t.out_row_stride + hl * t.out_head_stride;
-                    a[j].load(in + o0);
-                    if constexpr (kTwo)
-                        if (rotates) b[j].load(in + o1);
+        for (int j = 0; j < kBatch; ++j) {
+            tokens[j] = -1;
+            if (tok < here) {
+                const bool is_k = h >= p.q.heads;
+                const RopeTensor& t = is_k ? p.k : p.q;
+                const int hl = is_k ? h - p.q.heads : h;
+                const int64_t m = m0 + tok;
+                const T* in = static_cast<const T*>(t.in) + m * t.row_stride + hl * t.head_stride;
+                out[j] = static_cast<T*>(t.out) + m * t.out_row_stride + hl * t.out_head_stride;
+                a[j].load(in + o0);
+                if constexpr (kTwo)
+                    if (rotates) b[j].load(in + o1);
+                tokens[j] = tok;
+                h += p.head_lanes;
+                if (h >= heads) {
+                    h = h0;
+                    tok += slots;
                 }
             }
+        }
+    };
+    load();
+    for (int e = threadIdx.x; e < here * p.pairs; e += kRopeThreads) {
+        const int row = e / p.pairs, i = e - row * p.pairs;
+        const int64_t at = (m0 + row) * p.pos_row_stride + p.axis[i] * p.pos_axis_stride;
+        const double pos = p.pos64 ? static_cast<double>(static_cast<const int64_t*>(p.pos)[at])
+                                   : static_cast<double>(static_cast<const int32_t*>(p.pos)[at]);
+        const double turns = pos * p.inv_turn[i];
+        float s, c;
+        sincospif(2.0f * static_cast<float>(turns - rint(turns)), &s, &c);
+        table[e] = make_float2(c, p.inverse ? -s : s);
+    }
+    __syncthreads();
+    while (tokens[0] >= 0) {
 #pragma unroll
-            for (int j = 0; j < kHeads; ++j) {
-                if (hb + j * p.head_lanes >= heads) continue;
-                if (rotates) {
-                    float fa[VEC];
-                    a[j].get(fa);
-                    if constexpr (kTwo) {
-                        float fb[VEC];
-                        b[j].get(fb);
+        for (int j = 0; j < kBatch; ++j) {
+            if (tokens[j] < 0) continue;
+            if (rotates) {
+                float2 cs[kPairs];
 #pragma unroll
-                        for (int i = 0; i < VEC; ++i) {
-                            const float x = fa[i], y = fb[i];
-                            fa[i] = fmaf(x, cs[i].x, -(y * cs[i].y));
-                            fb[i] = fmaf(x, cs[i].y, y * cs[i].x);
-                        }
-                        b[j].set(fb);
-                        b[j].store(out[j] + o1);
-                    } else {
+                for (int i = 0; i < kPairs; ++i) cs[i] = table[tokens[j] * p.pairs + item * kPairs + i];
+                float fa[VEC];
+                a[j].get(fa);
+                if constexpr (kTwo) {
+                    float fb[VEC];
+                    b[j].get(fb);
 #pragma unroll
-                        for (int i = 0; i < kPairs; ++i) {
-                            const float x = fa[2 * i], y = fa[2 * i + 1];
-                            fa[2 * i] = fmaf(x, cs[i].x, -(y * cs[i].y));
-                            fa[2 * i + 1] = fmaf(x, cs[i].y, y * cs[i].x);
-                        }
+                    for (int i = 0; i < VEC; ++i) {
+                        const float x = fa[i], y = fb[i];
+                        fa[i] = fmaf(x, cs[i].x, -(y * cs[i].y));
+                        fb[i] = fmaf(x, cs[i].y, y * cs[i].x);
                     }
-                    a[j].set(fa);
+                    b[j].set(fb);
+                    b[j].store(out[j] + o1);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kPairs; ++i) {
+                        const float x = fa[2 * i], y = fa[2 * i + 1];
+                        fa[2 * i] = fmaf(x, cs[i].x, -(y * cs[i].y));
+                        fa[2 * i + 1] = fmaf(x, cs[i].y, y * cs[i].x);
+                    }
                 }
-                a[j].store(out[j] + o0);
+                a[j].set(fa);
             }
+            a[j].store(out[j] + o0);
         }
+        load();
     }
 }
 
