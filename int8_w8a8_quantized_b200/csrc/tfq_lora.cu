@@ -492,67 +492,123 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
 // Few rows (M <= kSmallM: a decoding step).  Everything is read once and
 // little is computed, so both kernels are built to have many loads in flight:
 //
-// lora_rows_kernel: t[m, r] = sum_k x[m,k] A[idx[m],r,k] / s_a[m] (fp32), one
-// dot product per `dot_warps` warps.
+// lora_rows_kernel: t[m, r] = sum_k x[m,k] A[idx[m],r,k] / s_a[m] (fp32), four
+// rows' dot products with their r-th factors per `dot_warps` warps.
 //
 // small_lora_kernel: the Linear with the weight as the tensor cores' M operand
 // (128 output channels per CTA) and the rows as N (rounded up to 16), so that a
 // tile is 128 channels wide however few rows there are, and K split over a
 // cluster: N / 128 tiles times the split reach all SMs.  While the weight
-// streams, the epilogue warps add up the adapters' second product on plain FMAs:
-// thread n reads Bs[a, n, :] of its channel once per row.  The partial sums of
-// the cluster meet in shared memory; CTA `rank` finishes its share of the rows.
+// streams, the epilogue's eight warps add up the adapters' second product on
+// plain FMAs: a thread has one channel n and reads Bs[a, n, :] once per row, 16
+// loads in flight.  The partial sums of the cluster meet in shared memory; CTA
+// `rank` finishes its share of the rows.
 constexpr int kSmallM = 64;
-constexpr int kSmallThreads = 192;
+constexpr int kSmallThreads = 64 + 256;
 constexpr int kSmallMaxStages = 6;
 
+// fp32 += the products of two 16-byte units of bf16.
+__device__ __forceinline__ float dot8(uint4 a, uint4 b, float s) {
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        s = fmaf(bf16_lo(x[i]), bf16_lo(y[i]), s);
+        s = fmaf(bf16_hi(x[i]), bf16_hi(y[i]), s);
+    }
+    return s;
+}
+
 __global__ void __launch_bounds__(256) lora_rows_kernel(const uint4* x, const uint4* A, const int32_t* idx,
-                                                        const float* s_a, int n_adapters, int R, int units,
+                                                        const float* s_a, int M, int n_adapters, int R, int units,
                                                         int dot_warps, float* t) {
-    __shared__ float sums[8];
+    constexpr int kRows = 4;
+    __shared__ float sums[8][kRows];
     // The wait comes first: a kernel that starts after every CTA here has allowed
     // it knows that all earlier kernels of the stream are complete.
     pdl_wait();
     pdl_allow_next();
     const int dots = 8 / dot_warps;  // per CTA; divides R
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t dot = static_cast<int64_t>(blockIdx.x) * dots + warp / dot_warps;
-    const int m = static_cast<int>(dot / R);
-    const int r = static_cast<int>(dot - static_cast<int64_t>(m) * R);
-    const uint32_t a = static_cast<uint32_t>(__ldg(idx + m));
-    if (a >= static_cast<uint32_t>(n_adapters)) return;  // the whole CTA has one row
-    const uint4* xr = x + static_cast<int64_t>(m) * units;
-    const uint4* ar = A + (static_cast<int64_t>(a) * R + r) * units;
-    float s = 0.0f;
-    const int step = 32 * dot_warps;
-#pragma unroll 1
-    for (int base = (warp % dot_warps) * 32 + lane; base < units; base += 8 * step) {
-        uint4 xv[8], av[8];
+    const int per_rows = R / dots;
+    const int m0 = static_cast<int>(blockIdx.x) / per_rows * kRows;
+    const int r = static_cast<int>(blockIdx.x) % per_rows * dots + warp / dot_warps;
+    const uint4* xr[kRows];
+    const uint4* ar[kRows];  // null: no row, or none with an adapter
+    bool same = true;
+    uint32_t first = 0xFFFFFFFFu;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int u = base + j * step;
-            xv[j] = u < units ? __ldg(xr + u) : make_uint4(0u, 0u, 0u, 0u);
-            av[j] = u < units ? ldg_nc_v4(ar + u) : make_uint4(0u, 0u, 0u, 0u);
+    for (int q = 0; q < kRows; ++q) {
+        const int m = m0 + q;
+        const uint32_t a = m < M ? static_cast<uint32_t>(__ldg(idx + m)) : 0xFFFFFFFFu;
+        const bool has = a < static_cast<uint32_t>(n_adapters);
+        xr[q] = x + static_cast<int64_t>(m) * units;
+        ar[q] = has ? A + (static_cast<int64_t>(a) * R + r) * units : nullptr;
+        if (has) {
+            if (first == 0xFFFFFFFFu) first = a;
+            same = same && a == first;
         }
+    }
+    if (first == 0xFFFFFFFFu) return;  // the whole CTA has these rows
+    const int step = 32 * dot_warps;
+    const int begin = (warp % dot_warps) * 32 + lane;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    float s[kRows] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (same) {  // the factor is read once for all rows
+        const uint4* shared_a = A + (static_cast<int64_t>(first) * R + r) * units;
+#pragma unroll 1
+        for (int base = begin; base < units; base += 3 * step) {
+            uint4 av[3], xv[kRows][3];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t xw[4] = {xv[j].x, xv[j].y, xv[j].z, xv[j].w}, aw[4] = {av[j].x, av[j].y, av[j].z, av[j].w};
+            for (int j = 0; j < 3; ++j) {
+                const int u = base + j * step;
+                av[j] = u < units ? ldg_nc_v4(shared_a + u) : zero;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                s = fmaf(bf16_lo(xw[i]), bf16_lo(aw[i]), s);
-                s = fmaf(bf16_hi(xw[i]), bf16_hi(aw[i]), s);
+                for (int q = 0; q < kRows; ++q) xv[q][j] = u < units && ar[q] != nullptr ? __ldg(xr[q] + u) : zero;
             }
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+#pragma unroll
+                for (int q = 0; q < kRows; ++q) s[q] = dot8(xv[q][j], av[j], s[q]);
+        }
+    } else {
+#pragma unroll 1
+        for (int base = begin; base < units; base += 2 * step) {
+            uint4 av[kRows][2], xv[kRows][2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int u = base + j * step;
+#pragma unroll
+                for (int q = 0; q < kRows; ++q) {
+                    const bool in = u < units && ar[q] != nullptr;
+                    av[q][j] = in ? ldg_nc_v4(ar[q] + u) : zero;
+                    xv[q][j] = in ? __ldg(xr[q] + u) : zero;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int q = 0; q < kRows; ++q) s[q] = dot8(xv[q][j], av[q][j], s[q]);
         }
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    for (int q = 0; q < kRows; ++q)
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s[q] += __shfl_xor_sync(0xFFFFFFFFu, s[q], o);
     if (dot_warps > 1) {
-        if (lane == 0) sums[warp] = s;
+        if (lane == 0)
+#pragma unroll
+            for (int q = 0; q < kRows; ++q) sums[warp][q] = s[q];
         __syncthreads();
         if (warp % dot_warps != 0) return;
-        for (int i = 1; i < dot_warps; ++i) s += sums[warp + i];
+        for (int i = 1; i < dot_warps; ++i)
+#pragma unroll
+            for (int q = 0; q < kRows; ++q) s[q] += sums[warp + i][q];
     }
-    if (lane == 0) t[dot] = __fdiv_rn(s, __ldg(s_a + m));
+    if (lane == 0) {
+#pragma unroll
+        for (int q = 0; q < kRows; ++q)
+            if (ar[q] != nullptr) t[static_cast<int64_t>(m0 + q) * R + r] = __fdiv_rn(s[q], __ldg(s_a + m0 + q));
+    }
 }
 
 struct SmallArgs {
@@ -573,6 +629,7 @@ struct SmallTail {
     uint64_t tmem_full;
     uint32_t tmem_slot;
     int abort_flag;
+    alignas(16) float t[2][4][TFQ_LORA_MAX_RANK];  // four rows' first product, for each half of the epilogue
 };
 
 __host__ __device__ constexpr int small_stage_bytes(int mn) { return (128 + mn) * BK; }
@@ -662,50 +719,61 @@ __global__ void __launch_bounds__(kSmallThreads)
             if (!mbar_wait(&s->tmem_full, 0, nullptr)) atomicOr(p.err, kErrGemmDrain);
         }
     } else {
-        const int quarter = warp & 3;
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
         const int nl = quarter * 32 + lane, n = n0 + nl;
         const int m0 = rank * p.share, m1 = min(p.M, m0 + p.share);
         pdl_wait();  // t
         const int units = p.R / 8;
-        for (int mb = m0; mb < m1; mb += 4) {
+        const int in_half = static_cast<int>(threadIdx.x) - 64 - 128 * half;
+        for (int mb = m0 + 4 * half; mb < m1; mb += 8) {
+            for (int e = in_half; e < p.R; e += 128)  // 4 R floats, 16 bytes at a time
+                if (mb + e / (p.R / 4) < m1)
+                    reinterpret_cast<float4*>(s->t[half][e / (p.R / 4)])[e % (p.R / 4)] =
+                        __ldg(reinterpret_cast<const float4*>(p.t + static_cast<int64_t>(mb) * p.R) + e);
+            named_bar_sync(1 + half, 128);
             const uint4* b[4];
-            const float4* t[4];
             float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const uint32_t a = mb + j < m1 ? static_cast<uint32_t>(__ldg(p.idx + mb + j)) : 0xFFFFFFFFu;
                 const bool has = a < static_cast<uint32_t>(p.n_adapters) && n < p.N;
                 b[j] = has ? p.Bs + (static_cast<int64_t>(a) * p.N + n) * units : nullptr;
-                t[j] = reinterpret_cast<const float4*>(p.t + static_cast<int64_t>(mb + j) * p.R);
             }
-#pragma unroll 2
-            for (int u = 0; u < units; ++u) {
-                uint4 v[4];
+            for (int u0 = 0; u0 < units; u0 += 4) {
+                uint4 v[4][4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (b[j] != nullptr) v[j] = __ldg(b[j] + u);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (b[j] == nullptr) continue;
-                    const float4 lo = __ldg(t[j] + 2 * u), hi = __ldg(t[j] + 2 * u + 1);
-                    acc[j] = fmaf(bf16_lo(v[j].x), lo.x, acc[j]);
-                    acc[j] = fmaf(bf16_hi(v[j].x), lo.y, acc[j]);
-                    acc[j] = fmaf(bf16_lo(v[j].y), lo.z, acc[j]);
-                    acc[j] = fmaf(bf16_hi(v[j].y), lo.w, acc[j]);
-                    acc[j] = fmaf(bf16_lo(v[j].z), hi.x, acc[j]);
-                    acc[j] = fmaf(bf16_hi(v[j].z), hi.y, acc[j]);
-                    acc[j] = fmaf(bf16_lo(v[j].w), hi.z, acc[j]);
-                    acc[j] = fmaf(bf16_hi(v[j].w), hi.w, acc[j]);
+                    for (int i = 0; i < 4; ++i)
+                        v[j][i] = b[j] != nullptr && u0 + i < units ? __ldg(b[j] + u0 + i) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (u0 + i >= units) break;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (b[j] == nullptr) continue;
+                        const float4 lo = reinterpret_cast<const float4*>(s->t[half][j])[2 * (u0 + i)];
+                        const float4 hi = reinterpret_cast<const float4*>(s->t[half][j])[2 * (u0 + i) + 1];
+                        acc[j] = fmaf(bf16_lo(v[j][i].x), lo.x, acc[j]);
+                        acc[j] = fmaf(bf16_hi(v[j][i].x), lo.y, acc[j]);
+                        acc[j] = fmaf(bf16_lo(v[j][i].y), lo.z, acc[j]);
+                        acc[j] = fmaf(bf16_hi(v[j][i].y), lo.w, acc[j]);
+                        acc[j] = fmaf(bf16_lo(v[j][i].z), hi.x, acc[j]);
+                        acc[j] = fmaf(bf16_hi(v[j][i].z), hi.y, acc[j]);
+                        acc[j] = fmaf(bf16_lo(v[j][i].w), hi.z, acc[j]);
+                        acc[j] = fmaf(bf16_hi(v[j][i].w), hi.w, acc[j]);
+                    }
                 }
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (mb + j < m1) lora[(mb + j - m0) * 128 + nl] = acc[j];
+            named_bar_sync(1 + half, 128);  // t is read
         }
         ok = mbar_wait_warp(&s->tmem_full, 0, abort_flag);
         if (ok) {
             tc_fence_after();
-            for (int c = 0; c < p.Mn; c += 16) {
+            for (int c = 16 * half; c < p.Mn; c += 32) {
                 uint32_t acc[16];
                 tmem_ld_32x32b_x16(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(c), acc);
                 tmem_ld_wait();
@@ -717,20 +785,28 @@ __global__ void __launch_bounds__(kSmallThreads)
             *abort_flag = 1;
             atomicOr(p.err, kErrLora);
         }
+        if (p.splits == 1) named_bar_sync(3, 256);  // the halves read each other's sums
     }
     __syncwarp();
     if (p.splits > 1) cluster_sync_all();  // every CTA's partial sums are written
     if (warp >= 2) {
-        const int nl = (warp & 3) * 32 + lane, n = n0 + nl;
+        const int nl = (warp & 3) * 32 + lane, n = n0 + nl, half = (warp - 2) >> 2;
         const int m0 = rank * p.share, m1 = min(p.M, m0 + p.share);
         if (n < p.N) {
             const float sw = __ldg(p.s_w + n);
             const float bias = p.bias != nullptr ? __bfloat162float(p.bias[n]) : 0.0f;
-            for (int m = m0; m < m1; ++m) {
+            for (int m = m0 + half; m < m1; m += 2) {
+                // rows 4 .. 7 of every eight are the other half's: the barriers behind that are passed
                 float v = lora[(m - m0) * 128 + nl];
                 const uint32_t at = smem_u32(part + m * 128 + nl);
                 if (p.splits > 1) {
-                    for (int q = 0; q < p.splits; ++q) v += ld_cluster_f32(mapa_shared(at, q));
+                    float w[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        if (q < p.splits) w[q] = ld_cluster_f32(mapa_shared(at, q));
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        if (q < p.splits) v += w[q];
                 } else {
                     v += part[m * 128 + nl];
                 }
@@ -802,14 +878,15 @@ tfq_status launch_shrink(const LoraCall& l, const float* s_a, int64_t M, int64_t
     a.t = t;
     a.err = ds->err_word;
     const int blocks = static_cast<int>((M + kShrinkRows - 1) / kShrinkRows);
-    // A CTA per 128 rows, more where rows of many adapters make more items and
-    // the grid is small; K over a cluster while every CTA keeps four steps.
-    // All of them are resident at once, two per SM.
+    // A CTA per 128 rows and one more, further ones where rows of many adapters
+    // make more items and the grid is small; K over a cluster while every CTA
+    // keeps four steps.  Those with work are resident at once, two per SM.
     const int block_rows = static_cast<int>(std::min<int64_t>(M, kShrinkRows));
-    const int least = (block_rows + 127) / 128;
-    const int items = std::min(block_rows, least + l.n_adapters - 1);
+    const int least = (block_rows + 127) / 128 + (l.n_adapters > 1 ? 1 : 0);  // a run's end makes one item more
+    const int items = std::min(block_rows, (block_rows + 127) / 128 + l.n_adapters - 1);
     a.splits = 1;
-    while (a.splits < 8 && blocks * least * a.splits * 2 <= 2 * ds->sm_count && a.k_blocks >= a.splits * 8)
+    while (a.splits < 8 && blocks * ((block_rows + 127) / 128) * a.splits * 2 <= 2 * ds->sm_count &&
+           a.k_blocks >= a.splits * 8)
         a.splits *= 2;
     a.item_ctas = std::max(least, std::min(items, 2 * ds->sm_count / (a.splits * blocks)));
     const int stage = shrink_stage_bytes(a.Rn);
@@ -851,11 +928,13 @@ tfq_status launch_small_lora(const void* A_q, const float* s_a, const void* W_q,
     const int units = static_cast<int>(K / 8);
     // warps per dot product: enough warps to keep the GPU's loads in flight, at least two loads a lane
     int dot_warps = 1;
-    while (dot_warps < 8 && M * l.R * dot_warps * 2 <= 32 * ds->sm_count && units >= 128 * dot_warps) dot_warps *= 2;
-    const int64_t ctas = M * l.R * dot_warps / 8;
+    while (dot_warps < 8 && (M + 3) / 4 * l.R * dot_warps * 2 <= 32 * ds->sm_count && units >= 64 * dot_warps)
+        dot_warps *= 2;
+    const int64_t ctas = (M + 3) / 4 * l.R * dot_warps / 8;
     tfq_status st = lora_launch_error(launch_cluster(lora_rows_kernel, static_cast<unsigned>(ctas), 256, 0, 1, stream,
                                                      static_cast<const uint4*>(l.x), static_cast<const uint4*>(l.A),
-                                                     l.idx, s_a, l.n_adapters, l.R, units, dot_warps, t));
+                                                     l.idx, s_a, static_cast<int>(M), l.n_adapters, l.R,
+                                                     units, dot_warps, t));
     if (st != TFQ_OK) return st;
     SmallArgs a = {};
     a.M = static_cast<int>(M);
