@@ -500,8 +500,8 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
 // tile is 128 channels wide however few rows there are, and K split over a
 // cluster: N / 128 tiles times the split reach all SMs.  While the weight
 // streams, the epilogue's eight warps add up the adapters' second product on
-// plain FMAs: a thread has one channel n and reads Bs[a, n, :] once per row, 16
-// loads in flight.  The partial sums of the cluster meet in shared memory; CTA
+// plain FMAs: a warp has 32 channels and reads their Bs[a, n, :] once per
+// row.  The partial sums of the cluster meet in shared memory; CTA
 // `rank` finishes its share of the rows.
 constexpr int kSmallM = 64;
 constexpr int kSmallThreads = 64 + 256;
@@ -632,9 +632,79 @@ struct SmallTail {
     alignas(16) float t[2][4][TFQ_LORA_MAX_RANK];  // four rows' first product, for each half of the epilogue
 };
 
+// The adapters' second product of up to four rows mb .. and a warp's 32 channels
+// from n_base: out[row * 128 + channel] = sum_r t[row][r] Bs[idx[mb + row], channel, r].
+// L neighbouring lanes share a channel's row of Bs, a 16-byte unit each, so that
+// the loads are consecutive (with a channel per lane they touched a line each,
+// and rank 64 took 7 us more than rank 16 on 16 x 5120 x 5120); a lane meets 32
+// channels in L passes, and the lanes' sums are joined by exchanging halves,
+// after which lane l holds one channel.
+template <int L>
+__device__ __forceinline__ void small_expand(const SmallArgs& p, const float (*t)[TFQ_LORA_MAX_RANK], int mb, int m1,
+                                             int n_base, int units, float* out) {
+    constexpr int kAtOnce = L == 1 ? 4 : 8 / L;  // rows in flight: up to 8 loads
+    const int lane = threadIdx.x & 31, c = lane % L, group = lane / L;
+#pragma unroll
+    for (int j0 = 0; j0 < 4; j0 += kAtOnce) {
+        if (mb + j0 >= m1) break;
+        int64_t row[kAtOnce];  // the adapter's first row of Bs, -1: none
+        float acc[kAtOnce][L];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            const uint32_t a = mb + j0 + j < m1 ? static_cast<uint32_t>(__ldg(p.idx + mb + j0 + j)) : 0xFFFFFFFFu;
+            row[j] = a < static_cast<uint32_t>(p.n_adapters) ? static_cast<int64_t>(a) * p.N : -1;
+#pragma unroll
+            for (int i = 0; i < L; ++i) acc[j][i] = 0.0f;
+        }
+        for (int u = c; u < (units + L - 1) / L * L; u += L) {
+            uint4 v[kAtOnce][L];
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j)
+#pragma unroll
+                for (int i = 0; i < L; ++i) {
+                    const int n = n_base + i * (32 / L) + group;
+                    v[j][i] = row[j] >= 0 && u < units && n < p.N ? __ldg(p.Bs + (row[j] + n) * units + u)
+                                                                  : make_uint4(0u, 0u, 0u, 0u);
+                }
+            if (u >= units) continue;
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+                if (row[j] < 0) continue;  // t was not written
+                const float4 lo = reinterpret_cast<const float4*>(t[j0 + j])[2 * u];
+                const float4 hi = reinterpret_cast<const float4*>(t[j0 + j])[2 * u + 1];
+#pragma unroll
+                for (int i = 0; i < L; ++i) {
+                    acc[j][i] = fmaf(bf16_lo(v[j][i].x), lo.x, acc[j][i]);
+                    acc[j][i] = fmaf(bf16_hi(v[j][i].x), lo.y, acc[j][i]);
+                    acc[j][i] = fmaf(bf16_lo(v[j][i].y), lo.z, acc[j][i]);
+                    acc[j][i] = fmaf(bf16_hi(v[j][i].y), lo.w, acc[j][i]);
+                    acc[j][i] = fmaf(bf16_lo(v[j][i].z), hi.x, acc[j][i]);
+                    acc[j][i] = fmaf(bf16_hi(v[j][i].z), hi.y, acc[j][i]);
+                    acc[j][i] = fmaf(bf16_lo(v[j][i].w), hi.z, acc[j][i]);
+                    acc[j][i] = fmaf(bf16_hi(v[j][i].w), hi.w, acc[j][i]);
+                }
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+#pragma unroll
+            for (int o = L / 2; o > 0; o >>= 1) {  // keep the passes with bit o as in c, give the others away
+#pragma unroll
+                for (int i = 0; i < o; ++i) {
+                    const float keep = (c & o) != 0 ? acc[j][i + o] : acc[j][i];
+                    const float give = (c & o) != 0 ? acc[j][i] : acc[j][i + o];
+                    acc[j][i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+                }
+            }
+            if (mb + j0 + j < m1) out[(j0 + j) * 128 + c * (32 / L) + group] = acc[j][0];
+        }
+    }
+}
+
 __host__ __device__ constexpr int small_stage_bytes(int mn) { return (128 + mn) * BK; }
 
-__global__ void __launch_bounds__(kSmallThreads)
+__global__ void __launch_bounds__(kSmallThreads, 2)  // all CTAs of a small grid resident
     small_lora_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                       const SmallArgs p) {
     extern __shared__ uint8_t smem_raw[];
@@ -720,7 +790,7 @@ __global__ void __launch_bounds__(kSmallThreads)
         }
     } else {
         const int quarter = warp & 3, half = (warp - 2) >> 2;
-        const int nl = quarter * 32 + lane, n = n0 + nl;
+        const int nl = quarter * 32 + lane;
         const int m0 = rank * p.share, m1 = min(p.M, m0 + p.share);
         pdl_wait();  // t
         const int units = p.R / 8;
@@ -731,43 +801,11 @@ __global__ void __launch_bounds__(kSmallThreads)
                     reinterpret_cast<float4*>(s->t[half][e / (p.R / 4)])[e % (p.R / 4)] =
                         __ldg(reinterpret_cast<const float4*>(p.t + static_cast<int64_t>(mb) * p.R) + e);
             named_bar_sync(1 + half, 128);
-            const uint4* b[4];
-            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t a = mb + j < m1 ? static_cast<uint32_t>(__ldg(p.idx + mb + j)) : 0xFFFFFFFFu;
-                const bool has = a < static_cast<uint32_t>(p.n_adapters) && n < p.N;
-                b[j] = has ? p.Bs + (static_cast<int64_t>(a) * p.N + n) * units : nullptr;
-            }
-            for (int u0 = 0; u0 < units; u0 += 4) {
-                uint4 v[4][4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        v[j][i] = b[j] != nullptr && u0 + i < units ? __ldg(b[j] + u0 + i) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (u0 + i >= units) break;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if (b[j] == nullptr) continue;
-                        const float4 lo = reinterpret_cast<const float4*>(s->t[half][j])[2 * (u0 + i)];
-                        const float4 hi = reinterpret_cast<const float4*>(s->t[half][j])[2 * (u0 + i) + 1];
-                        acc[j] = fmaf(bf16_lo(v[j][i].x), lo.x, acc[j]);
-                        acc[j] = fmaf(bf16_hi(v[j][i].x), lo.y, acc[j]);
-                        acc[j] = fmaf(bf16_lo(v[j][i].y), lo.z, acc[j]);
-                        acc[j] = fmaf(bf16_hi(v[j][i].y), lo.w, acc[j]);
-                        acc[j] = fmaf(bf16_lo(v[j][i].z), hi.x, acc[j]);
-                        acc[j] = fmaf(bf16_hi(v[j][i].z), hi.y, acc[j]);
-                        acc[j] = fmaf(bf16_lo(v[j][i].w), hi.z, acc[j]);
-                        acc[j] = fmaf(bf16_hi(v[j][i].w), hi.w, acc[j]);
-                    }
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (mb + j < m1) lora[(mb + j - m0) * 128 + nl] = acc[j];
+            float* to = lora + (mb - m0) * 128 + quarter * 32;
+            if (units >= 8) small_expand<8>(p, s->t[half], mb, m1, n0 + quarter * 32, units, to);
+            else if (units >= 4) small_expand<4>(p, s->t[half], mb, m1, n0 + quarter * 32, units, to);
+            else if (units >= 2) small_expand<2>(p, s->t[half], mb, m1, n0 + quarter * 32, units, to);
+            else small_expand<1>(p, s->t[half], mb, m1, n0 + quarter * 32, units, to);
             named_bar_sync(1 + half, 128);  // t is read
         }
         ok = mbar_wait_warp(&s->tmem_full, 0, abort_flag);
