@@ -349,10 +349,12 @@ struct LinearOperands {
 // The CTA-pair kernel with low-rank adapters beside the Linear (kLora): row m
 // adds sum_r t[m,r] Bs[a,n,r], a = idx[m], to its accumulator, with t and Bs in
 // units of the row's and the column's scale (tfq_lora.cu), so the epilogue's
-// s_a s_w covers both sums.  A tile's accumulator starts with one kind::f16
-// stage per adapter present in its 256 rows and 64 columns of the rank, then
-// takes the kind::f8f6f4 stages of the Linear.  The B operand of such a stage
-// is the adapter's Bs tile (TMA); the A operand is t with the rows of other
+// s_a s_w covers both sums.  A tile's accumulator starts with the kind::f16
+// stages of the adapters present in its 256 rows, then takes the kind::f8f6f4
+// stages of the Linear.  Such a stage holds 64 columns: those of one adapter's
+// rank, or the whole rank of two (R <= 32) or four (R <= 16) adapters side by
+// side as operand tiles of their own.  Its B operands are the adapters' Bs
+// tiles (TMA); the A operand is t with the rows of other
 // adapters zero, which four more warps per CTA write: a thread keeps its
 // row's t in registers and stores it to the stage of the row's own adapter,
 // zeros to the others.  (Measured on B200 with 12 adapters of rank 24 in any
@@ -370,8 +372,8 @@ struct LinearOperands {
 // when their tile begins.  The even producer leaves each stage's kind in
 // shared memory, and the MMA thread does what it says.
 struct LoraPairMaps : PairMaps {
-    CUtensorMap bs;   // Bs [n_adapters * N, R], 64 x PBN / 2 boxes
-    CUtensorMap bsq;  // ... 64 x PBN / 4 boxes (half-width tiles)
+    CUtensorMap bs;   // Bs [n_adapters * N, R], kLora x PBN / 2 boxes
+    CUtensorMap bsq;  // ... kLora x PBN / 4 boxes (half-width tiles)
     const int32_t* idx;
     const uint4* t;  // [M, R] bf16
     int n_adapters;
@@ -401,14 +403,24 @@ struct TileAdapters {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = row_adapter(idx, tm * 256 + lane * 8 + i, M, n_adapters);
     }
-    // The next adapter in increasing order, 0xFFFFFFFF past the last.  All lanes call it.
-    __device__ __forceinline__ uint32_t next() {
-        uint32_t a = 0xFFFFFFFFu;
+    // The next adapters in increasing order, at most `most` (up to 4) of them;
+    // how many.  All lanes call it.
+    __device__ __forceinline__ int next(uint32_t (&a)[4], int most) {
+        int n = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) a = min(a, v[i] >= from ? v[i] : 0xFFFFFFFFu);
-        a = __reduce_min_sync(0xFFFFFFFFu, a);
-        from = a + 1;
-        return a;
+        for (int j = 0; j < 4; ++j) {
+            a[j] = 0xFFFFFFFFu;
+            if (j < most && n == j) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) a[j] = min(a[j], v[i] >= from ? v[i] : 0xFFFFFFFFu);
+                a[j] = __reduce_min_sync(0xFFFFFFFFu, a[j]);
+                if (a[j] != 0xFFFFFFFFu) {
+                    from = a[j] + 1;
+                    ++n;
+                }
+            }
+        }
+        return n;
     }
 };
 
@@ -423,7 +435,7 @@ __device__ __forceinline__ bool lora_work_item(const GemmArgs& p, int w, int n_c
 }
 
 // The producer warp: the whole warp enumerates adapters, lane 0 issues.
-template <int PBN>
+template <int PBN, int kWidth>
 struct LoraProducer {
     using C = PairCfg<PBN>;
     const CUtensorMap& tmA;
@@ -450,19 +462,25 @@ struct LoraProducer {
         const int r_chunks = (maps.R + 63) / 64;
         const int b_rows = half < 0 ? C::kBHalf : C::kBHalf / 2;
         const int b_row = tn * PBN + (half > 0 ? PBN / 2 : 0) + rank * b_rows;
+        const uint32_t tile_bytes = static_cast<uint32_t>(b_rows * kWidth * 2);
+        const int steps = kWidth / 16;
         const CUtensorMap* map = half < 0 ? &maps.bs : &maps.bsq;
-        for (uint32_t a = present.next(); a != 0xFFFFFFFFu; a = present.next()) {
+        uint32_t a[4];
+        for (int n = present.next(a, 64 / kWidth); n > 0; n = present.next(a, 64 / kWidth)) {
             for (int c = 0; lane == 0 && c < r_chunks; ++c) {
                 const int st = stage();
                 if (st < 0) break;
                 mbar_arrive(&rows_go[st]);
                 const uint32_t full_leader = mapa_shared(smem_u32(&full[st]), 0);
                 if (rank == 0) {
-                    stage_info[st] = kStageLora | static_cast<uint32_t>(min(4, (maps.R - c * 64 + 15) / 16));
-                    mbar_arrive_expect_tx(&full[st], 2 * static_cast<uint32_t>(b_rows * BK));
+                    stage_info[st] = kStageLora | static_cast<uint32_t>((n - 1) * steps + min(steps, (maps.R - c * 64 + 15) / 16));
+                    mbar_arrive_expect_tx(&full[st], 2 * static_cast<uint32_t>(n) * tile_bytes);
                 }
-                tma_load_2d_pair(sB + st * C::kBStage, map, c * 64, static_cast<int>(a) * p.N + b_row, full_leader,
-                                 pol_b);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i < n)
+                        tma_load_2d_pair(sB + st * C::kBStage + i * tile_bytes, map, c * 64,
+                                         static_cast<int>(a[i]) * p.N + b_row, full_leader, pol_b);
                 ++it;
             }
         }
@@ -535,7 +553,7 @@ struct LoraProducer {
 // 128 has row i of this CTA's half.  The CTA's producer tells them through
 // rows_go when such a stage is free (they skip the Linear's stages, so they
 // could not follow the phases of "empty" themselves).
-template <int PBN>
+template <int PBN, int kWidth>
 __device__ __forceinline__ void lora_pair_rows(const LoraPairMaps& maps, const GemmArgs& p, uint8_t* sA,
                                                uint64_t* rows_go, uint64_t* rows_full,
                                                volatile int* abort_flag, int rank, int cluster, int n_clusters,
@@ -562,7 +580,8 @@ __device__ __forceinline__ void lora_pair_rows(const LoraPairMaps& maps, const G
                            : make_uint4(0u, 0u, 0u, 0u);
         };
         if (r_chunks == 1) fetch(0);
-        for (uint32_t a = present.next(); a != 0xFFFFFFFFu; a = present.next()) {
+        uint32_t a[4];
+        for (int n = present.next(a, 64 / kWidth); n > 0; n = present.next(a, 64 / kWidth)) {
             for (int c = 0; c < r_chunks; ++c, ++it) {
                 if (r_chunks > 1) fetch(c);
                 const int st = it % PAIR_STAGES;
@@ -571,11 +590,29 @@ __device__ __forceinline__ void lora_pair_rows(const LoraPairMaps& maps, const G
                     return;
                 }
                 phase ^= 1u << st;
-                uint8_t* dst = sA + st * C::kAStage + row * 128;
-                const bool keep = mine == a;
+                uint8_t* dst = sA + st * C::kAStage;
+                const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+                if constexpr (kWidth == 64) {  // 128-byte swizzle
 #pragma unroll
-                for (int u = 0; u < 8; ++u)  // 128-byte swizzle
-                    *reinterpret_cast<uint4*>(dst + ((u ^ (row & 7)) << 4)) = keep ? v[u] : make_uint4(0u, 0u, 0u, 0u);
+                    for (int u = 0; u < 8; ++u)
+                        *reinterpret_cast<uint4*>(dst + row * 128 + ((u ^ (row & 7)) << 4)) = mine == a[0] ? v[u] : zero;
+                } else if constexpr (kWidth == 32) {  // 64-byte swizzle: unit u of row r at u ^ (r / 2 % 4)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            if (i < n)
+                                *reinterpret_cast<uint4*>(dst + i * 8192 + row * 64 + ((u ^ ((row >> 1) & 3)) << 4)) =
+                                    mine == a[i] ? v[u] : zero;
+                } else {  // 32-byte swizzle: u ^ (r / 4 % 2)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+                            if (i < n)
+                                *reinterpret_cast<uint4*>(dst + i * 4096 + row * 32 + ((u ^ ((row >> 2) & 1)) << 4)) =
+                                    mine == a[i] ? v[u] : zero;
+                }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster_local_data(mapa_shared(smem_u32(&rows_full[st]), 0));
@@ -585,13 +622,15 @@ __device__ __forceinline__ void lora_pair_rows(const LoraPairMaps& maps, const G
     }
 }
 
-// The MMA thread of the even CTA.  It follows the producer's order: the first
+// The MMA warp of the even CTA.  It follows the producer's order: the first
 // tile's adapters, then for every tile its stages up to the last few, the next
 // tile's adapters, the rest.  How many stages the adapters take it reads from
 // shared memory, stage by stage; everything an instruction of the Linear needs
-// it knows per tile.  (Measured on B200: a loop that took accumulator and shape
-// from each stage's word instead ran 1.4 times as long.)
-template <int PBN>
+// it knows per tile.  The whole warp runs the loops and one lane issues, so
+// that addresses and descriptors live in uniform registers.  (Measured on B200:
+// a loop that took accumulator and shape from each stage's word ran 1.4 times
+// as long.)
+template <int PBN, int kWidth>
 struct LoraMma {
     using C = PairCfg<PBN>;
     const GemmArgs& p;
@@ -599,54 +638,75 @@ struct LoraMma {
     uint64_t *full, *empty, *order, *rows_full;
     const volatile uint32_t* stage_info;
     volatile int* abort_flag;
-    int it = 0;
+    bool leader;
+    int st = 0;               // the next stage and its phase
+    uint32_t phase = 0;
     uint32_t rows_phase = 0;  // a bit per stage
     bool ok = true;
 
     __device__ __forceinline__ bool wait_full() {
-        ok = ok && mbar_wait(&full[it % PAIR_STAGES], static_cast<uint32_t>(it / PAIR_STAGES) & 1u, abort_flag);
+        ok = ok && mbar_wait(&full[st], phase, abort_flag);
         return ok;
+    }
+    __device__ __forceinline__ void advance() {
+        if (++st == PAIR_STAGES) {
+            st = 0;
+            phase ^= 1u;
+        }
     }
 
     // The adapters' stages, if the next stage is one; true if there were any.
     __device__ __forceinline__ bool adapters(uint64_t* tmem_empty_bar, uint32_t empty_parity, uint32_t d_tmem, int n) {
         const uint32_t idesc = make_idesc_bf16(256, n);
-        uint32_t acc = 0;
+        // from one adapter's tile to the next, in 16-byte units
+        constexpr uint32_t kATile = 128u * kWidth * 2 / 16;
+        const uint32_t b_tile = static_cast<uint32_t>(n / 2) * (kWidth * 2 / 16);
+        bool any = false;
         while (wait_full()) {
-            const int st = it % PAIR_STAGES;
-            const uint32_t info = stage_info[st];
+            const uint32_t info = __shfl_sync(0xFFFFFFFFu, stage_info[st], 0);
             if ((info & kStageLora) == 0) break;
-            ok = acc != 0 || mbar_wait(tmem_empty_bar, empty_parity, abort_flag);
+            ok = any || mbar_wait(tmem_empty_bar, empty_parity, abort_flag);
             ok = ok && mbar_wait_cluster(&rows_full[st], (rows_phase >> st) & 1u, abort_flag);
             if (!ok) break;
             rows_phase ^= 1u << st;
             tc_fence_after();
-            const uint64_t a_desc = sw128_kmajor_desc(sA + st * C::kAStage);
-            const uint64_t b_desc = sw128_kmajor_desc(sB + st * C::kBStage);
+            const uint64_t a_desc = swizzled_kmajor_desc<kWidth * 2>(sA + st * C::kAStage);
+            const uint64_t b_desc = swizzled_kmajor_desc<kWidth * 2>(sB + st * C::kBStage);
+            const uint32_t steps = info & kStageSteps;
+            if (leader) {
 #pragma unroll
-            for (uint32_t k = 0; k < 4; ++k) {
-                if (k < (info & kStageSteps)) mma_bf16_pair(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc, acc);
-                acc = 1;
+                for (uint32_t k = 0; k < 4; ++k) {
+                    constexpr uint32_t kPer = kWidth / 16;  // instructions per adapter's tile, 32 bytes of a row each
+                    const uint64_t in_tile = 2 * (k % kPer);
+                    if (k < steps)
+                        mma_bf16_pair(d_tmem, a_desc + k / kPer * kATile + in_tile,
+                                      b_desc + k / kPer * b_tile + in_tile, idesc, (any || k > 0) ? 1u : 0u);
+                }
+                mma_commit_pair(&empty[st], 0x3);
             }
-            mma_commit_pair(&empty[st], 0x3);
-            ++it;
+            __syncwarp();
+            any = true;
+            advance();
         }
-        if (acc != 0) mma_commit_pair(order, 0x1);
-        return acc != 0;
+        if (any && leader) mma_commit_pair(order, 0x1);
+        return any;
     }
 
-    // Stages [kb0, kb1) of the Linear; acc0: the accumulator already holds something.
-    __device__ __forceinline__ void linear(int kb0, int kb1, uint32_t d_tmem, uint32_t idesc, bool acc0) {
-        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+    // `count` stages of the Linear; acc0: the accumulator already holds something.
+    __device__ __forceinline__ void linear(int count, uint32_t d_tmem, uint32_t idesc, bool acc0) {
+        for (int i = 0; i < count; ++i) {
             if (!wait_full()) return;
-            const int st = it % PAIR_STAGES;
             tc_fence_after();
             const uint64_t a_desc = sw128_kmajor_desc(sA + st * C::kAStage);
             const uint64_t b_desc = sw128_kmajor_desc(sB + st * C::kBStage);
+            if (leader) {
 #pragma unroll
-            for (int k = 0; k < BK / UMMA_K; ++k)
-                mma_e4m3_pair<false>(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc, (kb > 0 || k > 0 || acc0) ? 1u : 0u);
-            mma_commit_pair(&empty[st], 0x3);
+                for (int k = 0; k < BK / UMMA_K; ++k)
+                    mma_e4m3_pair<false>(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc, (i > 0 || k > 0 || acc0) ? 1u : 0u);
+                mma_commit_pair(&empty[st], 0x3);
+            }
+            __syncwarp();
+            advance();
         }
     }
 
@@ -671,24 +731,25 @@ struct LoraMma {
             }
             if (!ok) break;
             tc_fence_after();
-            linear(0, p.k_blocks - lead, d_tmem, idesc, after_lora);
+            linear(p.k_blocks - lead, d_tmem, idesc, after_lora);
             int half2 = -1;
             more = pair_work_item(w + n_clusters, total_tiles, n_clusters, p.tail_halves, t, half2);
             const bool after2 =
                 more && adapters(&tmem_empty[buf ^ 1], (static_cast<uint32_t>((c + 1) >> 1) & 1u) ^ 1u,
                                  tmem_base + static_cast<uint32_t>((buf ^ 1) * PBN), half2 < 0 ? PBN : PBN / 2);
-            linear(p.k_blocks - lead, p.k_blocks, d_tmem, idesc, after_lora);
-            if (ok) mma_commit_pair(&tmem_full[buf], 0x3);
+            linear(lead, d_tmem, idesc, true);
+            if (ok && leader) mma_commit_pair(&tmem_full[buf], 0x3);
             half = half2;
             after_lora = after2;
         }
     }
 };
 
-template <int PBN, int kAcc, int kQuant = 0, bool kLora = false>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads<kQuant, kLora>(), 1)
+// kLora: 0, or the columns of an adapter's tile (16, 32 or 64).
+template <int PBN, int kAcc, int kQuant = 0, int kLora = 0>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads<kQuant, kLora != 0>(), 1)
     scaled_mm_pair_kernel(const __grid_constant__ CUtensorMap tmA,
-                          const __grid_constant__ std::conditional_t<kLora, LoraPairMaps, PairMaps> maps,
+                          const __grid_constant__ std::conditional_t<kLora != 0, LoraPairMaps, PairMaps> maps,
                           GemmArgs p) {
     using C = PairCfg<PBN>;
     extern __shared__ uint8_t smem_raw[];
@@ -727,7 +788,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads<kQuant,
             mbar_init(&tmem_empty[i], 2 * EPI_WARPS);
         }
         mbar_init(drain, 1);
-        if constexpr (kLora) {
+        if constexpr (kLora != 0) {
             mbar_init(order, 1);
             for (int i = 0; i < PAIR_STAGES; ++i) {
                 mbar_init(&rows_full[i], 2 * LORA_WARPS);
@@ -756,8 +817,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads<kQuant,
 
     if (warp == 0) {
         // ---------------------------------------------------- TMA producer
-        if constexpr (kLora) {
-            LoraProducer<PBN> producer = {tmA,        maps,       p,
+        if constexpr (kLora != 0) {
+            LoraProducer<PBN, kLora> producer = {tmA,        maps,       p,
                                           sA,         sB,         full,
                                           empty,      rows_go,    stage_info,
                                           abort_flag, static_cast<int>(rank), lane};
@@ -818,13 +879,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads<kQuant,
         }
     } else if (warp == 1) {
         // ------------------------------------------- MMA issuer (even CTA)
-        if constexpr (kLora) {
-            if (lane == 0 && rank == 0) {
-                LoraMma<PBN> mma = {p, sA, sB, full, empty, order, rows_full, stage_info, abort_flag};
+        if constexpr (kLora != 0) {
+            if (rank == 0) {
+                const bool leader = elect_one();
+                LoraMma<PBN, kLora> mma = {p,     sA,        sB,         full,       empty, order,
+                                           rows_full, stage_info, abort_flag, leader};
                 mma.run(tmem_full, tmem_empty, tmem_base, cluster, n_clusters);
-                if (!mma.ok) give_up(abort_flag, p.err, kErrGemmMma);
-                mma_commit_pair(drain, 0x1);
-                if (!mbar_wait(drain, 0, nullptr)) atomicOr(p.err, kErrGemmDrain);
+                if (leader) {
+                    if (!mma.ok) give_up(abort_flag, p.err, kErrGemmMma);
+                    mma_commit_pair(drain, 0x1);
+                    if (!mbar_wait(drain, 0, nullptr)) atomicOr(p.err, kErrGemmDrain);
+                }
             }
         } else if (lane == 0 && rank == 0) {
             int it = 0, tcount = 0, t, half;
@@ -916,9 +981,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads<kQuant,
         }
         if (lane == 0) bulk_wait<0>();
         __syncwarp();
-    } else if constexpr (kLora) {
+    } else if constexpr (kLora != 0) {
         // ------------------------------------ row warps of the adapters
-        lora_pair_rows<PBN>(maps, p, sA, rows_go, rows_full, abort_flag, static_cast<int>(rank), cluster, n_clusters,
+        lora_pair_rows<PBN, kLora>(maps, p, sA, rows_go, rows_full, abort_flag, static_cast<int>(rank), cluster, n_clusters,
                             static_cast<int>(threadIdx.x) - THREADS, lane);
     } else {
         // ------------------------------------ quantizer warps (kQuant only)
@@ -1187,10 +1252,17 @@ tfq_status launch_lora_pair_gemm(const void* A, const float* s_a, const void* W,
                                  cudaStream_t stream, DeviceState* ds) {
     constexpr int kPBN = 256;
     using C = PairCfg<kPBN>;
-    auto kernel = scaled_mm_pair_kernel<kPBN, kAccF32, 0, true>;
+    const int width = l.R <= 16 ? 16 : l.R <= 32 ? 32 : 64;
+    auto kernel = width == 64   ? scaled_mm_pair_kernel<kPBN, kAccF32, 0, 64>
+                  : width == 32 ? scaled_mm_pair_kernel<kPBN, kAccF32, 0, 32>
+                                : scaled_mm_pair_kernel<kPBN, kAccF32, 0, 16>;
     if (!ds->lora_attr_set) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(C::kSmemLora));
+        cudaError_t e = cudaSuccess;
+        for (auto k : {scaled_mm_pair_kernel<kPBN, kAccF32, 0, 16>, scaled_mm_pair_kernel<kPBN, kAccF32, 0, 32>,
+                       scaled_mm_pair_kernel<kPBN, kAccF32, 0, 64>})
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(C::kSmemLora));
         if (e != cudaSuccess) return fail(TFQ_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
         ds->lora_attr_set = true;
     }
@@ -1204,8 +1276,11 @@ tfq_status launch_lora_pair_gemm(const void* A, const float* s_a, const void* W,
     st = pair_linear_setup(&lin, 1, M, K, maps, a);
     const auto bf16_map = [&](CUtensorMap* m, const void* base, int64_t rows, uint32_t box_rows) {
         if (st == TFQ_OK)
-            st = encode_tensor_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, l.R, rows, l.R * 2, 64, box_rows,
-                                      CU_TENSOR_MAP_SWIZZLE_128B);
+            st = encode_tensor_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, l.R, rows, l.R * 2,
+                                      static_cast<uint32_t>(width), box_rows,
+                                      width == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
+                                      : width == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                    : CU_TENSOR_MAP_SWIZZLE_32B);
     };
     bf16_map(&maps.bs, l.Bs, l.n_adapters * N, C::kBHalf);
     bf16_map(&maps.bsq, l.Bs, l.n_adapters * N, C::kBHalf / 2);

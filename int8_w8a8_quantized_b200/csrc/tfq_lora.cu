@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
 // plain FMAs: a warp has 32 channels and reads their Bs[a, n, :] once per
 // row.  The partial sums of the cluster meet in shared memory; CTA
 // `rank` finishes its share of the rows.
-constexpr int kSmallM = 64;
+constexpr int kSmallM = 128;
 constexpr int kSmallThreads = 64 + 256;
 constexpr int kSmallMaxStages = 6;
 
@@ -716,7 +716,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2)  // all CTAs of a small grid
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = p.splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int n0 = static_cast<int>(blockIdx.x) / p.splits * 128;
-    const uint32_t tmem_cols = p.Mn <= 32 ? 32 : 64;
+    const uint32_t tmem_cols = p.Mn <= 32 ? 32 : p.Mn <= 64 ? 64 : 128;
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.stages; ++i) {
             mbar_init(&s->full[i], 1);
@@ -996,10 +996,14 @@ tfq_status launch_small_lora(const void* A_q, const float* s_a, const void* W_q,
     a.share = static_cast<int>((M + a.splits - 1) / a.splits);
     const int rest = 1024 + a.share * 512 + static_cast<int>(sizeof(SmallTail));
     const int stage = small_stage_bytes(a.Mn);
-    a.stages = std::min(kSmallMaxStages, (112 * 1024 - rest) / stage);  // two CTAs per SM
+    // as many stages as leave room for two CTAs per SM, but two, and enough to
+    // hold the partial sums afterwards (a short K is not split, and one CTA then
+    // has all rows' second product: that may take more than half an SM)
+    const int least = std::max(2, (a.Mn * 512 + stage - 1) / stage);
+    a.stages = std::max(least, std::min(kSmallMaxStages, (112 * 1024 - rest) / stage));
     const size_t smem = static_cast<size_t>(rest) + static_cast<size_t>(a.stages) * stage;
     if (!ds->small_attr_set) {
-        const cudaError_t e = cudaFuncSetAttribute(small_lora_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 112 * 1024);
+        const cudaError_t e = cudaFuncSetAttribute(small_lora_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
         if (e != cudaSuccess) return fail(TFQ_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
         ds->small_attr_set = true;
     }
@@ -1015,6 +1019,14 @@ tfq_status launch_small_lora(const void* A_q, const float* s_a, const void* W_q,
 
 }  // namespace
 
+// Few rows.  Its cost grows with M R, that of the path for many rows with the
+// adapters that meet in a tile.  Measured on B200, 5120 x 5120 (us, few against
+// many): M = 64, R = 64, one adapter 25 / 32, 64 of them 29 / 88; M = 96, R = 32
+// 25 / 31 and 29 / 92; M = 96, R = 64 36 / 32 and 44 / 96.
+static bool use_small_lora(int64_t M, int64_t R, int64_t n_adapters) {
+    return M <= 64 || (M <= kSmallM && (M * R <= 4096 || n_adapters > 8));
+}
+
 // The first product: bf16 [M, R], or fp32 for few rows.
 size_t lora_workspace_bytes(int64_t M, int64_t R) { 
     return static_cast<size_t>(M) * static_cast<size_t>(R) * (M <= kSmallM ? 4 : 2);
@@ -1023,7 +1035,7 @@ size_t lora_workspace_bytes(int64_t M, int64_t R) {
 tfq_status launch_scaled_fp8_lora(const void* A_q, const float* s_a, const void* W_q, const float* s_w,
                                   const void* bias, int64_t M, int64_t N, int64_t K, const LoraCall& l, void* out,
                                   cudaStream_t stream, DeviceState* ds) {
-    if (M <= kSmallM) return launch_small_lora(A_q, s_a, W_q, s_w, bias, M, N, K, l, out, stream, ds);
+    if (use_small_lora(M, l.R, l.n_adapters)) return launch_small_lora(A_q, s_a, W_q, s_w, bias, M, N, K, l, out, stream, ds);
     __nv_bfloat16* t = static_cast<__nv_bfloat16*>(l.workspace);
     tfq_status st = launch_shrink(l, s_a, M, K, t, stream, ds);
     if (st != TFQ_OK) return st;

@@ -220,6 +220,13 @@ __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // ----------------------------------------------------------------- cluster
 __device__ __forceinline__ uint32_t cluster_ctarank() {
     uint32_t r;
@@ -417,6 +424,15 @@ __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.
 __device__ __forceinline__ uint64_t sw128_kmajor_desc(const void* smem_tile) {
     const uint64_t addr = smem_u32(smem_tile);
     return ((addr >> 4) & 0x3FFFull) | (1ull << 16) | ((1024ull >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// The same for rows of 32, 64 or 128 bytes written with the swizzle of that span
+// (modes 6, 4, 2), 8-row groups 8 rows apart; base aligned to 1024 bytes.
+template <int kRowBytes>
+__device__ __forceinline__ uint64_t swizzled_kmajor_desc(const void* smem_tile) {
+    constexpr uint64_t mode = kRowBytes == 128 ? 2 : kRowBytes == 64 ? 4 : 6;
+    return ((static_cast<uint64_t>(smem_u32(smem_tile)) >> 4) & 0x3FFFull) | (1ull << 16) |
+           (static_cast<uint64_t>(8 * kRowBytes >> 4) << 32) | (1ull << 46) | (mode << 61);
 }
 
 }  // namespace tfq

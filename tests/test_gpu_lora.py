@@ -77,6 +77,8 @@ CASES = [  # M, N, K, R, adapters
     (1025, 776, 2064, 64, 33), (2500, 520, 1040, 200, 5), (4111, 264, 272, 24, 100),
     (9000, 2056, 272, 24, 6), (5000, 4104, 784, 72, 3), (33, 24, 16, 8, 2), (48, 13824, 512, 256, 5),
     (1300, 64, 144, 8, 1000), (70, 72, 4096, 256, 3), (513, 328, 2064, 248, 70),
+    (700, 264, 528, 32, 9), (1025, 520, 272, 8, 33), (100, 1032, 784, 64, 20), (128, 264, 528, 24, 30),
+    (3000, 2056, 528, 16, 3), (129, 264, 144, 48, 9),
 ]
 
 
