@@ -280,15 +280,53 @@ __device__ __forceinline__ bool x_rows(ShrinkTail& s, const ShrinkArgs& p, uint8
     return true;
 }
 
+// Adds the S CTAs' partial sums of this CTA's share of the item's rows, in rank
+// order, and writes them to t (the epilogue's 128 threads; several remote loads
+// of each in flight).
+template <int S>
+__device__ __forceinline__ void join_parts(const ShrinkArgs& p, const float* part, const ShrinkItems& item, int row0,
+                                           int rank) {
+    constexpr int kShare = 128 / S, kBatch = S <= 4 ? 4 / S : 1;
+    const int units = p.R / 4;
+    const int rows = min(kShare, item.len - rank * kShare);
+    const int n = rows * units;  // 16-byte units of this share, negative or 0: none
+    uint32_t base[S];
+#pragma unroll
+    for (int q = 0; q < S; ++q) base[q] = mapa_shared(smem_u32(part), q);
+    for (int e0 = threadIdx.x - 64; e0 < n; e0 += 128 * kBatch) {
+        float4 v[kBatch][S];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int e = e0 + 128 * b, i = rank * kShare + e / units, u = e % units;
+            if (e < n)
+#pragma unroll
+                for (int q = 0; q < S; ++q) v[b][q] = ld_cluster_v4(base[q] + (i * (p.R + 4) + 4 * u) * 4);
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int e = e0 + 128 * b, i = rank * kShare + e / units, u = e % units;
+            if (e >= n) break;
+            float4 s = v[b][0];
+#pragma unroll
+            for (int q = 1; q < S; ++q) s = make_float4(s.x + v[b][q].x, s.y + v[b][q].y, s.z + v[b][q].z, s.w + v[b][q].w);
+            const int m = row0 + item.row(i);
+            const float sa = __ldg(p.s_a + m);
+            *reinterpret_cast<uint2*>(p.t + static_cast<int64_t>(m) * p.R + 4 * u) =
+                make_uint2(pack2(__fdiv_rn(s.x, sa), __fdiv_rn(s.y, sa)), pack2(__fdiv_rn(s.z, sa), __fdiv_rn(s.w, sa)));
+        }
+    }
+}
+
 __global__ void __launch_bounds__(kShrinkThreads, 2)
     lora_shrink_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmA,
                        const ShrinkArgs p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int stage_bytes = shrink_stage_bytes(p.Rn);
-    float* part = reinterpret_cast<float*>(smem + p.stages * stage_bytes);  // [128][R], splits > 1
-    ShrinkTail* s = reinterpret_cast<ShrinkTail*>(reinterpret_cast<uint8_t*>(part) +
-                                                  (p.splits > 1 ? 128 * p.R * sizeof(float) : 0));
+    // splits > 1: an item's partial sums [128][R + 4] (padded so that a warp's
+    // rows spread over the banks), in the stages' memory once they are consumed
+    float* part = reinterpret_cast<float*>(smem);
+    ShrinkTail* s = reinterpret_cast<ShrinkTail*>(smem + p.stages * stage_bytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = p.splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int unit = blockIdx.x / p.splits;
@@ -424,11 +462,9 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
 #pragma unroll
                         for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(acc[8 * h + j]);
                         if (p.splits > 1) {
-                            // 16-byte units of a row rotated by the row, so that a warp's rows spread over the banks
-                            const int units = p.R / 4;
-                            float4* dst = reinterpret_cast<float4*>(part + i * p.R);
-                            dst[((c + 8 * h) / 4 + i) % units] = make_float4(f[0], f[1], f[2], f[3]);
-                            dst[((c + 8 * h) / 4 + 1 + i) % units] = make_float4(f[4], f[5], f[6], f[7]);
+                            float4* dst = reinterpret_cast<float4*>(part + i * (p.R + 4) + c + 8 * h);
+                            dst[0] = make_float4(f[0], f[1], f[2], f[3]);
+                            dst[1] = make_float4(f[4], f[5], f[6], f[7]);
                         } else {
 #pragma unroll
                             for (int j = 0; j < 8; ++j) f[j] = __fdiv_rn(f[j], sa);
@@ -447,25 +483,10 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
             __syncwarp();
             cluster_sync_all();
             if (warp >= 2) {
-                const int share = 128 / p.splits, units = p.R / 4;
-                for (int e = threadIdx.x - 64; e < share * units; e += 128) {
-                    const int i = rank * share + e / units, u = e % units;
-                    if (i >= item.len) break;
-                    const uint32_t at = smem_u32(reinterpret_cast<float4*>(part + i * p.R) + (u + i) % units);
-                    float4 w[8];
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        if (q < p.splits) w[q] = ld_cluster_v4(mapa_shared(at, q));
-                    float4 v = w[0];
-#pragma unroll
-                    for (int q = 1; q < 8; ++q)
-                        if (q < p.splits) v = make_float4(v.x + w[q].x, v.y + w[q].y, v.z + w[q].z, v.w + w[q].w);
-                    const int m = row0 + item.row(i);
-                    const float sa = __ldg(p.s_a + m);
-                    *reinterpret_cast<uint2*>(p.t + static_cast<int64_t>(m) * p.R + 4 * u) =
-                        make_uint2(pack2(__fdiv_rn(v.x, sa), __fdiv_rn(v.y, sa)),
-                                   pack2(__fdiv_rn(v.z, sa), __fdiv_rn(v.w, sa)));
-                }
+                if (p.splits == 2) join_parts<2>(p, part, item, row0, rank);
+                else if (p.splits == 4) join_parts<4>(p, part, item, row0, rank);
+                else join_parts<8>(p, part, item, row0, rank);
+                fence_proxy_async_smem();  // the next item's copies write here
             }
             __syncwarp();
             cluster_sync_all();  // nobody overwrites or leaves what another still reads
@@ -928,15 +949,11 @@ tfq_status launch_shrink(const LoraCall& l, const float* s_a, int64_t M, int64_t
         a.splits *= 2;
     a.item_ctas = std::max(least, std::min(items, 2 * ds->sm_count / (a.splits * blocks)));
     const int stage = shrink_stage_bytes(a.Rn);
-    int rest = 1024 + static_cast<int>(sizeof(ShrinkTail)) + (a.splits > 1 ? 128 * a.R * 4 : 0);
-    if (rest + 2 * stage > 227 * 1024) {  // the largest rank: no room for partial sums
-        a.splits = 1;
-        rest = 1024 + static_cast<int>(sizeof(ShrinkTail));
-    }
-    // two CTAs per SM where two stages fit half the shared memory
-    const int budget = rest + 2 * stage <= 112 * 1024 ? 112 * 1024 : 227 * 1024;
-    a.stages = std::min(kShrinkMaxStages, (budget - rest) / stage);
-    if (a.stages < 2) return fail(TFQ_EUNSUPPORTED, "rank %d does not fit shared memory", l.R);
+    const int rest = 1024 + static_cast<int>(sizeof(ShrinkTail));
+    // as many stages as leave room for two CTAs per SM, but two, and enough to
+    // hold an item's partial sums afterwards (the largest ranks: one CTA per SM)
+    const int least_stages = std::max(2, a.splits > 1 ? (128 * (a.R + 4) * 4 + stage - 1) / stage : 0);
+    a.stages = std::max(least_stages, std::min(kShrinkMaxStages, (112 * 1024 - rest) / stage));
     const size_t smem = static_cast<size_t>(rest) + static_cast<size_t>(a.stages) * stage;
     if (!ds->shrink_attr_set) {
         const cudaError_t e = cudaFuncSetAttribute(lora_shrink_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
