@@ -1045,7 +1045,7 @@ static bool use_small_lora(int64_t M, int64_t R, int64_t n_adapters) {
 }
 
 // The first product: bf16 [M, R], or fp32 for few rows.
-size_t lora_workspace_bytes(int64_t M, int64_t R) { 
+size_t lora_workspace_bytes(int64_t M, int64_t R) {
     return static_cast<size_t>(M) * static_cast<size_t>(R) * (M <= kSmallM ? 4 : 2);
 }
 

@@ -627,6 +627,21 @@ struct RingRow {
     }
 };
 
+// A warp's bounded wait for a row slot, and what it does after giving up: it
+// records that, its thread that issues the copies (if it has one) waits out
+// those of the next `in_flight` slots, and the warp leaves its rows.
+__device__ __forceinline__ bool ring_wait(uint64_t* full, uint32_t phase) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(full, phase, nullptr));
+}
+__device__ __forceinline__ void ring_give_up(uint64_t* full, int slot, int slots, uint32_t phase, bool issuer,
+                                             int64_t in_flight, uint32_t* err) {
+    atomicOr(err, kErrNorm);
+    for (int i = 0; issuer && i < slots && i < in_flight; ++i) {
+        const bool wrapped = slot + i >= slots;
+        mbar_wait(&full[wrapped ? slot + i - slots : slot + i], phase ^ (wrapped ? 1u : 0u), nullptr);
+    }
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
@@ -742,8 +757,8 @@ __global__ void __launch_bounds__(kMaxThreads, kMaxThreads <= kRingSmall ? 2 : 1
             for (int i = 0; i < P; ++i)  // a column past the row gives 0, which no maximum sees
                 if (!valid[i / (VEC / 2)]) w[i] = make_float2(0.0f, 0.0f);
         }
-        if (!mbar_wait(&s.full[slot], phase, nullptr)) {
-            atomicOr(err, kErrNorm);
+        if (!ring_wait(&s.full[slot], phase)) {  // the barriers below do not count warps that have left
+            ring_give_up(s.full, slot, slots, phase, t == 0, last - r, err);
             break;
         }
         float2 x[P];
@@ -869,8 +884,8 @@ __global__ void __launch_bounds__(kMaxThreads, kMaxThreads <= kRingSmall ? 2 : 1
     for (int64_t r = first; r < last; ++r) {
         const float next_mean = r + 1 < last ? __ldg(p.mean + r + 1) : 0.0f;
         const float next_rstd = r + 1 < last ? __ldg(p.rstd + r + 1) : 0.0f;
-        if (!mbar_wait(&full[slot], phase, nullptr)) {
-            atomicOr(err, kErrNorm);
+        if (!ring_wait(&full[slot], phase)) {
+            ring_give_up(full, slot, slots, phase, t == 0, last - r, err);
             break;
         }
         const uint8_t* src = ring + static_cast<size_t>(slot) * 2 * row_bytes;
@@ -1011,8 +1026,12 @@ __global__ void __launch_bounds__(32 * kRowWarps, 1) norm_rows_kernel(const Norm
     int slot = 0, par = 0;
     uint32_t phase = 0;
     for (int64_t r = first; r < last; r += step, par ^= 1) {
-        if (!mbar_wait(&full[row][slot], phase, nullptr)) {
-            atomicOr(err, kErrNorm);
+        if (!ring_wait(&full[row][slot], phase)) {
+            ring_give_up(full[row], slot, slots, phase, place == 0, r + step < last ? 2 : 1, err);
+            if constexpr (W == 2) {  // the row's other warp is or will be at its barrier: it leaves too
+                if (lane == 0) joined[par][row][sub][1] = -1.0f;
+                row_sync();
+            }
             break;
         }
         float2 x[P];
@@ -1057,6 +1076,10 @@ __global__ void __launch_bounds__(32 * kRowWarps, 1) norm_rows_kernel(const Norm
                 joined[par][row][sub][1] = m2;
             }
             row_sync();
+            if (joined[par][row][sub ^ 1][1] < 0.0f) {  // no sum of squares: the other warp gave up
+                ring_give_up(full[row], slot, slots, phase, place == 0, r + step < last ? 2 : 1, err);
+                break;
+            }
             // both warps get the same bits: the terms are added in the warps' order
             const float s0 = joined[par][row][0][0], s1 = joined[par][row][1][0];
             mean = (s0 + s1) * inv_k;
@@ -1199,9 +1222,9 @@ NormKernel forward_kernel(const NormShape& s) {
     constexpr int V = 16 / sizeof(T);
     if (s.vec) {
         if (s.block == 256 && s.tpr <= 32) return norm_forward_kernel<T, V, 2, true, kQuant>;
-        return s.j == 2   ? norm_forward_kernel<T, V, 2, false, kQuant>
-               : s.j == 4 ? norm_forward_kernel<T, V, 4, false, kQuant>
-                          : norm_forward_kernel<T, V, 8, false, kQuant>;
+        // between these and the longest rows lie the ring's
+        constexpr int kMid = sizeof(T) == 4 ? 2 : 4;
+        return s.j == kMid ? norm_forward_kernel<T, V, kMid, false, kQuant> : norm_forward_kernel<T, V, 8, false, kQuant>;
     }
     if (s.block == 256 && s.tpr <= 32) return norm_forward_kernel<T, 1, 2, true, kQuant>;
     if (s.j == 2) return norm_forward_kernel<T, 1, 2, false, kQuant>;
@@ -1213,9 +1236,8 @@ NormKernel backward_kernel(const NormShape& s) {
     constexpr int V = 16 / sizeof(T);
     if (s.vec) {
         if (s.block == 256 && s.tpr <= 32) return norm_backward_kernel<T, V, 2, true>;
-        return s.j == 2   ? norm_backward_kernel<T, V, 2, false>
-               : s.j == 4 ? norm_backward_kernel<T, V, 4, false>
-                          : norm_backward_kernel<T, V, 8, false>;
+        constexpr int kMid = sizeof(T) == 4 ? 2 : 4;
+        return s.j == kMid ? norm_backward_kernel<T, V, kMid, false> : norm_backward_kernel<T, V, 8, false>;
     }
     if (s.block == 256 && s.tpr <= 32) return norm_backward_kernel<T, 1, 2, true>;
     if (s.j == 2) return norm_backward_kernel<T, 1, 2, false>;
