@@ -310,7 +310,9 @@ TFQ_API tfq_status tfq_mxfp8_linear(const void *A_q, const void *sf_a, const voi
  * (Additions of this library; the pages name the Linear only.)  In these
  * entry points x, dy, q, k and what has their type may be strided and need
  * only their own element's alignment where so stated: 16-byte accesses are
- * used where every row allows them, element accesses otherwise.
+ * used where every row allows them, element accesses otherwise.  Outputs and
+ * workspaces overlap neither one another nor an input, but where a call may
+ * be in place.
  * ------------------------------------------------------------------------
  *
  * tfq_layer_norm: for row m of group g = m / (M / groups),
@@ -324,7 +326,7 @@ TFQ_API tfq_status tfq_mxfp8_linear(const void *A_q, const void *sf_a, const voi
  *   weight, bias : [groups, K] dense, of `w_dtype` (dtype or TFQ_DTYPE_FP32),
  *            or NULL (a missing weight multiplies by 1 whatever weight_offset is,
  *            a missing bias is 0); element-aligned.
- *   y      : [M, K] dense, of `dtype`, written.
+ *   y      : [M, K] dense, of `dtype`, written; may be x itself (x_stride == K).
  *   mean, rstd : [M] fp32, written, or both NULL.
  * Statistics are fp32; the variance is summed from x - mean.  NaN or inf in a
  * row makes that row of y NaN (or inf) and no other.  eps == 0 is allowed (a
@@ -430,7 +432,10 @@ TFQ_API tfq_status tfq_rope_axes(const void *q, int64_t q_row_stride, int64_t q_
  *       s_a and s_w must be positive (the quantizers' are).
  *   x_bf16  : [M, K] bf16, the activations the codes A_q were made from.
  *   lora_A  : [n_adapters, R, K] bf16;  lora_Bs : [n_adapters, N, R] bf16, made
- *       once per weight by tfq_lora_fold (below): lora_B in units of s_w.
+ *       once per weight by tfq_lora_fold (below): lora_B in units of s_w.  Its
+ *       values must be finite (tfq_lora_fold's are): the tensor cores multiply
+ *       the adapters of neighbouring rows by zero.  Anything else that is inf
+ *       or NaN (a row of x, an adapter's lora_A) reaches the rows that use it.
  *   adapter : [M] int32, one adapter per row, in any order (rows of one request
  *       one after the other run fastest); a value outside [0, n_adapters)
  *       means no adapter for that row.
@@ -457,7 +462,9 @@ TFQ_API tfq_status tfq_scaled_fp8_linear_lora(const void *A_q, const float *s_a,
 
 /*
  * tfq_lora_fold: lora_Bs[a,n,r] = bf16_rn(scaling[a] * lora_B[a,n,r] / s_w[n])
- * (fp32 product and quotient), once per adapter and weight.
+ * (fp32 product and quotient), once per adapter and weight.  A result that is
+ * not finite is stored as the largest finite bf16 of its sign (NaN: the
+ * positive one), so that a broken adapter shows in its own rows alone.
  *   lora_B, lora_Bs : [n_adapters, N, R] bf16 (lora_Bs may be lora_B: in place);
  *   scaling : [n_adapters] fp32 or NULL (1);  s_w : [N] fp32.
  * Errors: TFQ_EINVAL (negative sizes, a null or misaligned pointer: 2 bytes for

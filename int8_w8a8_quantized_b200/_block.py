@@ -150,6 +150,8 @@ def _affine(weight, bias, x, K, device):
     given = weight if weight is not None else bias
     if given is None:
         return 1, x.dtype
+    if not isinstance(given, torch.Tensor):
+        raise TypeError("weight and bias must be torch.Tensors")
     if given.dtype is not x.dtype and given.dtype is not torch.float32:
         raise TypeError(f"weight and bias must be {x.dtype} or torch.float32, got {given.dtype}")
     groups = given.shape[0] if given.dim() == 2 else 1
@@ -176,7 +178,8 @@ def tfq_layer_norm(x, weight=None, bias=None, eps: float = 1e-6, weight_offset: 
     strided): (x - mean) * rstd * (weight + weight_offset) + bias.  weight and
     bias: [K], or [G, K] for G equal groups of consecutive rows (an adaptive
     norm's scale, with weight_offset 1, and shift), of x's type or fp32, or None.
-    Returns y, with stats=True (y, mean, rstd) (fp32 [M], what the gradient needs)."""
+    Returns y, with stats=True (y, mean, rstd) (fp32 [M], what the gradient needs).
+    y=x (contiguous) normalizes in place."""
     stride = _rows(x, "x")
     dtype = _norm_type(x)
     dev = x.get_device()
