@@ -528,11 +528,12 @@ __global__ void __launch_bounds__(J > 4 ? 1024 : 512)
 }
 
 // dw[g, c] = sum over i of part_dw[g][i][c], and db likewise: 32 columns per
-// CTA, the parts split over 8 warps and joined in order.
+// CTA, the parts split over its warps and joined in order.
+constexpr int kPartWarps = 32;
 template <typename T>
-__global__ void __launch_bounds__(256) norm_partials_kernel(const float* part_dw, const float* part_db, int K,
+__global__ void __launch_bounds__(32 * kPartWarps) norm_partials_kernel(const float* part_dw, const float* part_db, int K,
                                                             int parts, int w_f32, void* dw, void* db) {
-    __shared__ float sums[8][33];
+    __shared__ float sums[kPartWarps][33];
     pdl_allow_next();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -546,14 +547,14 @@ __global__ void __launch_bounds__(256) norm_partials_kernel(const float* part_dw
     if (c < K) {
         const float* at = part + g * parts * K + c;
 #pragma unroll 8
-        for (int i = warp; i < parts; i += 8) s += at[static_cast<int64_t>(i) * K];
+        for (int i = warp; i < parts; i += kPartWarps) s += at[static_cast<int64_t>(i) * K];
     }
     sums[warp][lane] = s;
     __syncthreads();
     if (warp == 0 && c < K) {
         s = sums[0][lane];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) s += sums[i][lane];
+        for (int i = 1; i < kPartWarps; ++i) s += sums[i][lane];
         if (w_f32) static_cast<float*>(dst)[g * K + c] = s;
         else static_cast<T*>(dst)[g * K + c] = from_float<T>(s);
     }
@@ -1451,7 +1452,7 @@ tfq_status launch_layer_norm_backward(const NormCall& c, const void* dy, int64_t
     auto join = c.dtype == TFQ_DTYPE_FP32 ? norm_partials_kernel<float>
                 : c.dtype == TFQ_DTYPE_FP16 ? norm_partials_kernel<__half> : norm_partials_kernel<__nv_bfloat16>;
     const dim3 jgrid(static_cast<unsigned>((c.K + 31) / 32 * c.groups), 2);
-    return launch_error("layer norm gradient", launch_kernel(join, jgrid, dim3(256), 0, stream,
+    return launch_error("layer norm gradient", launch_kernel(join, jgrid, dim3(32 * kPartWarps), 0, stream,
                                                              const_cast<const float*>(a.part_dw),
                                                              const_cast<const float*>(a.part_db), a.K, a.parts,
                                                              a.w_f32, dw, db));
