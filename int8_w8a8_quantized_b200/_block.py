@@ -89,15 +89,24 @@ def _codes(t, name, device):
         raise ValueError(f"{name} must be contiguous")
 
 
+# Outputs are allocated in the cheapest form (a call with few rows is bound by such
+# steps): empty_like takes 1.4 us, new_empty of an int 1.6, of a shape with a type 2 to 2.4.
+def _like(t, dtype=None):
+    """A new contiguous tensor of t's shape."""
+    return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
+
+
 def _output(t, name, dtype, shape, like):
-    if t is None:
-        return like.new_empty(shape, dtype=dtype)
-    return _dense(t, name, dtype, shape, like.get_device())
+    if t is not None:
+        return _dense(t, name, dtype, shape, like.get_device())
+    if like.shape == shape:
+        return _like(like, dtype)
+    return like.new_empty(*shape, dtype=dtype)
 
 
 def _workspace(t, need, like):
     if t is None:
-        return like.new_empty((need,), dtype=torch.uint8)
+        return like.new_empty(need, dtype=torch.uint8)
     _operand(t, "workspace", torch.uint8, 1, like.get_device())
     if t.numel() < need or not t.is_contiguous():
         raise ValueError(f"workspace must hold {need} contiguous bytes")
@@ -188,7 +197,8 @@ def tfq_layer_norm(x, weight=None, bias=None, eps: float = 1e-6, weight_offset: 
     y = _output(y, "y", x.dtype, (M, K), x)
     mean = rstd = None
     if stats:
-        mean, rstd = x.new_empty((2, M), dtype=torch.float32).unbind(0)
+        mean = x.new_empty(M, dtype=torch.float32)
+        rstd = _like(mean)
     _call("tfq_layer_norm", dev, x.data_ptr(), stride, dtype, _ptr(weight), _ptr(bias), _DTYPES[wdt], weight_offset,
           M, K, groups, eps, y.data_ptr(), _ptr(mean), _ptr(rstd))
     return (y, mean, rstd) if stats else y
@@ -239,7 +249,6 @@ def tfq_layer_norm_backward(dy, x, weight, mean, rstd, weight_offset: float = 0.
         if dweight_dtype is not None and dweight_dtype is not weight.dtype:
             raise TypeError("dweight_dtype differs from weight's")
         groups, wdt = _affine(weight, None, x, K, dev)
-        shape = weight.shape
     else:
         wdt = x.dtype if dweight_dtype is None else dweight_dtype
         if wdt is not x.dtype and wdt is not torch.float32:
@@ -249,9 +258,11 @@ def tfq_layer_norm_backward(dy, x, weight, mean, rstd, weight_offset: float = 0.
         if groups < 1 or M % groups:
             raise ValueError(f"{M} rows do not make {groups} equal groups")
         need_weight = False
-    dx = x.new_empty((M, K)) if need_x else None
-    dw = x.new_empty(shape, dtype=wdt) if need_weight else None
-    db = x.new_empty(shape, dtype=wdt) if need_bias else None
+    dx = _like(x) if need_x else None
+    dw = _like(weight) if need_weight else None
+    db = None
+    if need_bias:
+        db = x.new_empty(*shape, dtype=wdt) if weight is None else _like(weight)
     if need_weight or need_bias:
         workspace = _workspace(workspace, tfq_layer_norm_backward_workspace_bytes(M, K, groups), x)
     else:
@@ -291,7 +302,7 @@ def _heads(t, name, dtype, device, M, D):
 
 def _rope_output(out, name, like, device):
     if out is None:
-        return like.new_empty(like.shape)
+        return _like(like)
     _heads(out, name, like.dtype, device, like.shape[0], like.shape[2])
     if out.shape[1] != like.shape[1]:
         raise ValueError(f"{name} must have {like.shape[1]} heads")
