@@ -286,7 +286,7 @@ __device__ __forceinline__ bool x_rows(ShrinkTail& s, const ShrinkArgs& p, uint8
 template <int S>
 __device__ __forceinline__ void join_parts(const ShrinkArgs& p, const float* part, const ShrinkItems& item, int row0,
                                            int rank) {
-    constexpr int kShare = 128 / S, kBatch = S <= 4 ? 4 / S : 1;
+    constexpr int kShare = 128 / S, kBatch = S == 2 ? 4 : 1;
     const int units = p.R / 4;
     const int rows = min(kShare, item.len - rank * kShare);
     const int n = rows * units;  // 16-byte units of this share, negative or 0: none
@@ -295,12 +295,14 @@ __device__ __forceinline__ void join_parts(const ShrinkArgs& p, const float* par
     for (int q = 0; q < S; ++q) base[q] = mapa_shared(smem_u32(part), q);
     for (int e0 = threadIdx.x - 64; e0 < n; e0 += 128 * kBatch) {
         float4 v[kBatch][S];
+        float sa[kBatch];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
             const int e = e0 + 128 * b, i = rank * kShare + e / units, u = e % units;
-            if (e < n)
+            if (e >= n) break;
+            sa[b] = __ldg(p.s_a + row0 + item.row(i));
 #pragma unroll
-                for (int q = 0; q < S; ++q) v[b][q] = ld_cluster_v4(base[q] + (i * (p.R + 4) + 4 * u) * 4);
+            for (int q = 0; q < S; ++q) v[b][q] = ld_cluster_v4(base[q] + (i * (p.R + 4) + 4 * u) * 4);
         }
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
@@ -310,9 +312,9 @@ __device__ __forceinline__ void join_parts(const ShrinkArgs& p, const float* par
 #pragma unroll
             for (int q = 1; q < S; ++q) s = make_float4(s.x + v[b][q].x, s.y + v[b][q].y, s.z + v[b][q].z, s.w + v[b][q].w);
             const int m = row0 + item.row(i);
-            const float sa = __ldg(p.s_a + m);
             *reinterpret_cast<uint2*>(p.t + static_cast<int64_t>(m) * p.R + 4 * u) =
-                make_uint2(pack2(__fdiv_rn(s.x, sa), __fdiv_rn(s.y, sa)), pack2(__fdiv_rn(s.z, sa), __fdiv_rn(s.w, sa)));
+                make_uint2(pack2(__fdiv_rn(s.x, sa[b]), __fdiv_rn(s.y, sa[b])),
+                           pack2(__fdiv_rn(s.z, sa[b]), __fdiv_rn(s.w, sa[b])));
         }
     }
 }
@@ -480,16 +482,16 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
         }
         if (p.splits > 1) {
             // every CTA's partial sums are in its shared memory: CTA `rank` adds up its share of the rows
+            fence_proxy_async_smem();  // the next item's copies write there
             __syncwarp();
             cluster_sync_all();
             if (warp >= 2) {
                 if (p.splits == 2) join_parts<2>(p, part, item, row0, rank);
                 else if (p.splits == 4) join_parts<4>(p, part, item, row0, rank);
                 else join_parts<8>(p, part, item, row0, rank);
-                fence_proxy_async_smem();  // the next item's copies write here
             }
             __syncwarp();
-            cluster_sync_all();  // nobody overwrites or leaves what another still reads
+            cluster_sync_after_reads();  // nobody overwrites or leaves what another still reads
         }
     }
     if (warp == 0 && lane == 0) {  // loads in flight must land before the CTA leaves
@@ -874,7 +876,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2)  // all CTAs of a small grid
         }
     }
     __syncwarp();
-    if (p.splits > 1) cluster_sync_all();  // nobody leaves while its partial sums are read
+    if (p.splits > 1) cluster_sync_after_reads();  // nobody leaves while its partial sums are read
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {

@@ -254,6 +254,14 @@ __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
+// The cluster's threads wait for one another where nothing they wrote is read by
+// another CTA afterwards: the values read before are in registers and have been
+// used.  (The releasing arrive above waits for the thread's global stores, 2400
+// cycles behind some.)
+__device__ __forceinline__ void cluster_sync_after_reads() {
+    asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
 // 2-D tiled tensor load into this CTA's shared memory whose completion is
 // counted on an mbarrier of either CTA of the pair (cta_group::2).
 __device__ __forceinline__ void tma_load_2d_pair(void* smem_dst, const CUtensorMap* map, int32_t x, int32_t y,
