@@ -410,7 +410,7 @@ TFQ_API tfq_status tfq_layer_norm_backward(const void *dy, int64_t dy_stride, co
  * Errors: TFQ_EINVAL (negative sizes, unknown type or pairing, n_pairs < 1 or
  * 2 n_pairs > D, n_axes < 1, an axis out of range, inv_freq not finite, a null
  * or not element-aligned pointer), TFQ_EUNSUPPORTED (D > TFQ_ROPE_MAX_D,
- * q_heads + k_heads > 65536, M >= 2^31, not sm_100).
+ * n_axes > 255, q_heads + k_heads > 65536, M >= 2^31, not sm_100).
  */
 #define TFQ_ROPE_MAX_D 256
 #define TFQ_ROPE_MAX_PAIRS 128

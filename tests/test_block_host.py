@@ -108,6 +108,7 @@ LORA = dict(A_q=P, s_a=P, W_q=P, s_w=P, bias=None, M=4, N=16, K=32, x=P, A=P, Bs
 @pytest.mark.parametrize("change,status", [
     (dict(K=24), INVAL), (dict(N=12), INVAL), (dict(M=-1), INVAL), (dict(A_q=None), INVAL), (dict(n=-1), INVAL),
     (dict(R=-8), INVAL), (dict(R=12), INVAL), (dict(R=264), UNSUP), (dict(n=1 << 28), UNSUP),
+    (dict(n=(1 << 22) + 1), UNSUP), (dict(n=1 << 22, N=512), UNSUP), (dict(n=1 << 16, N=32768), UNSUP),
     (dict(x=None), INVAL), (dict(A=None), INVAL), (dict(Bs=None), INVAL), (dict(idx=None), INVAL),
     (dict(ws=None), INVAL), (dict(x=P + 8), INVAL), (dict(A=P + 8), INVAL), (dict(Bs=P + 2), INVAL),
     (dict(idx=P + 2), INVAL), (dict(ws=P + 4), INVAL), (dict(M=0, x=None), OK), (dict(N=0, Bs=None), OK),
@@ -178,3 +179,11 @@ def test_package_lists_the_operators():
         assert name in tfq.__all__ and name in dir(tfq) and callable(getattr(tfq, name))
     with pytest.raises(AttributeError):
         tfq.no_such_operator
+
+
+def test_only_tensors_are_operands():
+    x = torch.zeros((4, 32))
+    for call in (lambda: tfq.tfq_layer_norm(x), lambda: tfq.tfq_layer_norm([1.0]), lambda: tfq.tfq_rope_axes(x, None, x, x, x),
+                 lambda: tfq.tfq_lora_fold(x, None, x), lambda: tfq.tfq_layer_norm(x, stream=0)):
+        with pytest.raises((TypeError, ValueError)):
+            call()

@@ -318,3 +318,34 @@ def test_fold_never_stores_inf_or_nan():
     big = torch.finfo(torch.bfloat16).max
     want = torch.tensor([big, -big, big, big, -big, 0.0, 6e20, -1.5e20], device="cuda")
     assert torch.equal(Bs[0], want.bfloat16()[:, None].expand(8, 8))
+
+
+@pytest.mark.parametrize("M,K", [(7, 96), (60, 1001), (33, 1536), (5000, 1536), (3, 20000)])
+def test_bias_without_weight(M, K):
+    """A missing weight multiplies by 1, whatever its offset; groups come from the bias."""
+    g = torch.Generator(device="cuda").manual_seed(K)
+    G = 3 if M % 3 == 0 else 1
+    x = torch.randn((M, K), generator=g, device="cuda")
+    b = torch.randn((G, K), generator=g, device="cuda")
+    y = tfq.tfq_layer_norm(x, None, b, weight_offset=5.0)
+    want = tfq.tfq_layer_norm(x, torch.ones_like(b), b)
+    assert torch.equal(y, want)
+    if K % 16 == 0:
+        q, s = tfq.tfq_layer_norm_quant_fp8(x, None, b, weight_offset=5.0)
+        q1, s1 = tfq.tfq_layer_norm_quant_fp8(x, torch.ones_like(b), b)
+        assert torch.equal(q, q1) and torch.equal(s, s1)
+
+
+def test_refusals_on_the_gpu():
+    x = torch.zeros((4, 32), device="cuda")
+    w = torch.zeros(32, device="cuda")
+    with pytest.raises(TypeError):
+        tfq.tfq_layer_norm(x, 1.0)
+    with pytest.raises(ValueError):
+        tfq.tfq_layer_norm(x, w[:16])
+    with pytest.raises(ValueError):
+        tfq.tfq_layer_norm(x, w, stream=torch.cuda.current_stream(), y=x[:2])
+    with pytest.raises(ValueError):
+        tfq.tfq_layer_norm(x.cpu(), w)
+    with pytest.raises(ValueError):
+        tfq.tfq_layer_norm(x, w.cpu())
