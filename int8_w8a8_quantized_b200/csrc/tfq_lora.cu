@@ -47,12 +47,14 @@ __global__ void __launch_bounds__(256) lora_fold_kernel(const __nv_bfloat16* B, 
 // adapter, which the block's `item_ctas` CTAs share out.  An item is a
 // [128, K] x [K, Rn] product on the tensor cores (Rn = R rounded up to 16):
 // its x rows come as one TMA box where they are consecutive, else row by row
-// through the registers of the epilogue's warps, which are idle then; either
+// as asynchronous copies that the epilogue's warps, idle then, issue; either
 // way every row of x is read once, and A once per item (from L2).  (Measured
 // on B200, 12 adapters of rank 64 in any order, 9472 x 5120: streaming a
 // tile's x once for two adapters at a time and keeping each row's own product
-// 242 us, TMA gathers of four rows 116 us (some 56 cycles each), cp.async
-// 163 us (the fence behind each step waits for all copies in flight).)  Bound
+// 242 us, TMA gathers of four rows 116 us (some 56 cycles each), rows through
+// the warps' registers 85 us, asynchronous copies 64 us; with the fence between
+// copies and tensor cores behind each step's copies, where it waits for all of
+// them, instead of in front of the step's MMAs 163 us.)  Bound
 // by HBM: 2 R flops per value of x are far below the tensor cores' ratio; they
 // are used because plain FMAs would not keep up.
 // Few rows split K over a cluster of S CTAs, whose partial sums meet in
@@ -79,7 +81,7 @@ struct ShrinkArgs {
 // Shared memory behind the stages and, with splits > 1, the partial sums.
 struct ShrinkTail {
     uint64_t full[kShrinkMaxStages], empty[kShrinkMaxStages];
-    uint64_t x_full[kShrinkMaxStages];  // x rows that came through registers
+    uint64_t x_full[kShrinkMaxStages];  // x rows copied one by one
     uint64_t tmem_full, tmem_empty, drain;
     uint32_t tmem_slot;
     int abort_flag;
@@ -224,58 +226,33 @@ __device__ __forceinline__ void order_rows(ShrinkTail& s, int n_adapters, bool i
     }
 }
 
-// The x rows of an item of up to 16 * NP rows, by the epilogue's 128 threads:
-// eight threads a row, 16 rows at a time, 8 / NP steps of K at once, and the
-// next such batch in flight while the present one is stored: 16 loads a thread
-// whatever the item's rows.  False after giving up.
-template <int NP>
+// The x rows of an item that are not consecutive, by the epilogue's 128 threads:
+// eight threads a row, 16 rows at a time, as asynchronous copies on whose
+// completion the stage's x_full counts.  The threads only issue: nothing waits
+// for the data but the MMA thread, which also makes it visible to the tensor
+// cores.  False after giving up.
 __device__ __forceinline__ bool x_rows(ShrinkTail& s, const ShrinkArgs& p, uint8_t* smem, const ShrinkItems& item,
                                        int row0, int kb0, int kb1, int& it) {
-    constexpr int kSteps = 8 / NP;
-    const int lane = threadIdx.x & 31, chunk = threadIdx.x & 7, sub = (threadIdx.x - 64) >> 3;
+    const int chunk = threadIdx.x & 7, sub = (threadIdx.x - 64) >> 3;
     const int stage_bytes = shrink_stage_bytes(p.Rn);
-    const __nv_bfloat16* src[NP];
+    const __nv_bfloat16* src[8];
 #pragma unroll
-    for (int j = 0; j < NP; ++j) {
+    for (int j = 0; j < 8; ++j) {
         const int r = sub + 16 * j;
         src[j] = r < item.len ? p.x + static_cast<int64_t>(row0 + item.row(r)) * p.K + chunk * 8 : nullptr;
     }
-    const auto load = [&](uint4(&v)[8], int kb) {
+    // 128-byte swizzle; rows 16 apart have the same unit
+    const uint32_t dst0 = smem_u32(smem) + static_cast<uint32_t>(sub * 128 + ((chunk ^ (sub & 7)) << 4));
+    for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        const int st = it % p.stages;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&s.empty[st], (static_cast<uint32_t>(it / p.stages) & 1u) ^ 1u, &s.abort_flag)))
+            return false;
+        const bool in = kb * 64 + chunk * 8 < p.K;  // zeros past the row's end
+        const uint32_t dst = dst0 + static_cast<uint32_t>(st * stage_bytes);
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            const bool in = kb + i < kb1 && (kb + i) * 64 + chunk * 8 < p.K;
-#pragma unroll
-            for (int j = 0; j < NP; ++j)
-                v[i * NP + j] = in && src[j] != nullptr ? ldg_nc_v4(reinterpret_cast<const uint4*>(src[j] + (kb + i) * 64))
-                                                        : make_uint4(0u, 0u, 0u, 0u);
-        }
-    };
-    const auto store = [&](const uint4(&v)[8], int kb) {
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            if (kb + i >= kb1) break;
-            const int st = it % p.stages;
-            if (!mbar_wait_warp(&s.empty[st], (static_cast<uint32_t>(it / p.stages) & 1u) ^ 1u, &s.abort_flag)) return false;
-            uint8_t* sx = smem + st * stage_bytes;
-#pragma unroll
-            for (int j = 0; j < NP; ++j) {  // 128-byte swizzle
-                const int r = sub + 16 * j;
-                if (src[j] != nullptr) *reinterpret_cast<uint4*>(sx + r * 128 + ((chunk ^ (r & 7)) << 4)) = v[i * NP + j];
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.x_full[st]);
-            ++it;
-        }
-        return true;
-    };
-    uint4 v0[8], v1[8];
-    load(v0, kb0);
-    for (int kb = kb0; kb < kb1; kb += 2 * kSteps) {
-        load(v1, kb + kSteps);
-        if (!store(v0, kb)) return false;
-        load(v0, kb + 2 * kSteps);
-        if (!store(v1, kb + kSteps)) return false;
+        for (int j = 0; j < 8; ++j)
+            if (src[j] != nullptr) cp_async_16(dst + j * 2048, in ? src[j] + kb * 64 : src[j], in ? 16u : 0u);
+        cp_async_arrive(&s.x_full[st]);
     }
     return true;
 }
@@ -342,7 +319,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
         for (int i = 0; i < p.stages; ++i) {
             mbar_init(&s->full[i], 1);
             mbar_init(&s->empty[i], 1);
-            mbar_init(&s->x_full[i], 4);
+            mbar_init(&s->x_full[i], 128);
         }
         mbar_init(&s->tmem_full, 1);
         mbar_init(&s->tmem_empty, 4);
@@ -416,6 +393,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
                     if (ok && !box) {
                         ok = mbar_wait(&s->x_full[st], (x_phase >> st) & 1u, abort_flag);
                         x_phase ^= 1u << st;
+                        fence_proxy_async_smem();
                     }
                     if (!ok) break;
                     tc_fence_after();
@@ -441,11 +419,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
             if (item.box() || !ok) {
                 it += kb1 - kb0;
             } else {
-                const int passes = (item.len + 15) / 16;
-                if (passes > 4) ok = x_rows<8>(*s, p, smem, item, row0, kb0, kb1, it);
-                else if (passes > 2) ok = x_rows<4>(*s, p, smem, item, row0, kb0, kb1, it);
-                else if (passes > 1) ok = x_rows<2>(*s, p, smem, item, row0, kb0, kb1, it);
-                else ok = x_rows<1>(*s, p, smem, item, row0, kb0, kb1, it);
+                ok = x_rows(*s, p, smem, item, row0, kb0, kb1, it);
             }
             if (ok) ok = mbar_wait_warp(&s->tmem_full, turn & 1u, abort_flag);
             if (ok) {
@@ -501,6 +475,8 @@ __global__ void __launch_bounds__(kShrinkThreads, 2)
     } else if (warp == 1 && lane == 0) {
         mma_commit(&s->drain);
         if (!mbar_wait(&s->drain, 0, nullptr)) atomicOr(p.err, kErrGemmDrain);
+    } else if (warp >= 2) {
+        cp_async_wait_all();
     }
     tc_fence_before();
     __syncthreads();
