@@ -296,7 +296,7 @@ __device__ __forceinline__ void join_parts(const ShrinkArgs& p, const float* par
     }
 }
 
-__global__ void __launch_bounds__(kShrinkThreads, 2)
+__global__ void __launch_bounds__(kShrinkThreads, 3)
     lora_shrink_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmA,
                        const ShrinkArgs p) {
     extern __shared__ uint8_t smem_raw[];
@@ -917,21 +917,27 @@ tfq_status launch_shrink(const LoraCall& l, const float* s_a, int64_t M, int64_t
     const int blocks = static_cast<int>((M + kShrinkRows - 1) / kShrinkRows);
     // A CTA per 128 rows and one more, further ones where rows of many adapters
     // make more items and the grid is small; K over a cluster while every CTA
-    // keeps four steps.  Those with work are resident at once, two per SM.
+    // keeps four steps.  Those with work are resident at once.
     const int block_rows = static_cast<int>(std::min<int64_t>(M, kShrinkRows));
     const int least = (block_rows + 127) / 128 + (l.n_adapters > 1 ? 1 : 0);  // a run's end makes one item more
     const int items = std::min(block_rows, (block_rows + 127) / 128 + l.n_adapters - 1);
+    // Three CTAs per SM where that leaves three stages each: more of them share a
+    // block's items (12 adapters of rank 24 in any order, 1777 x 5120: 29 us
+    // against 36 with two).  Higher ranks would be left with two stages (rank 64,
+    // the whole call on 9472 x 5120 x 5120, two against three CTAs: one adapter
+    // 233 / 243 us, four in any order 251 / 265, 64 of them 757 / 725).
+    const int per_sm = a.Rn <= 32 ? 3 : 2;
     a.splits = 1;
     while (a.splits < 8 && blocks * ((block_rows + 127) / 128) * a.splits * 2 <= 2 * ds->sm_count &&
            a.k_blocks >= a.splits * 8)
         a.splits *= 2;
-    a.item_ctas = std::max(least, std::min(items, 2 * ds->sm_count / (a.splits * blocks)));
+    a.item_ctas = std::max(least, std::min(items, per_sm * ds->sm_count / (a.splits * blocks)));
     const int stage = shrink_stage_bytes(a.Rn);
     const int rest = 1024 + static_cast<int>(sizeof(ShrinkTail));
-    // as many stages as leave room for two CTAs per SM, but two, and enough to
-    // hold an item's partial sums afterwards (the largest ranks: one CTA per SM)
+    // as many stages as leave room for them, but two, and enough to hold an
+    // item's partial sums afterwards (the largest ranks: one CTA per SM)
     const int least_stages = std::max(2, a.splits > 1 ? (128 * (a.R + 4) * 4 + stage - 1) / stage : 0);
-    a.stages = std::max(least_stages, std::min(kShrinkMaxStages, (112 * 1024 - rest) / stage));
+    a.stages = std::max(least_stages, std::min(kShrinkMaxStages, ((per_sm == 3 ? 75 : 112) * 1024 - rest) / stage));
     const size_t smem = static_cast<size_t>(rest) + static_cast<size_t>(a.stages) * stage;
     if (!ds->shrink_attr_set) {
         const cudaError_t e = cudaFuncSetAttribute(lora_shrink_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
