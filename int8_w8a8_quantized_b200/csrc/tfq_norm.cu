@@ -529,8 +529,8 @@ __global__ void __launch_bounds__(J > 4 ? 1024 : 512)
 
 // dw[g, c] = sum over i of part_dw[g][i][c], and db likewise: 32 columns per
 // CTA, the parts split over its warps and joined in order.  (Bound by latency:
-// 7 us for 1036 parts of 1536 columns; with 8 warps the backward of 32760 x
-// 1536 took 81 us instead of 71.)
+// 7 us for 888 parts of 1536 columns; with 8 warps the backward of 32760 x
+// 1536 took 10 us longer.)
 constexpr int kPartWarps = 32;
 template <typename T>
 __global__ void __launch_bounds__(32 * kPartWarps) norm_partials_kernel(const float* part_dw, const float* part_db, int K,
@@ -844,8 +844,8 @@ __global__ void __launch_bounds__(kMaxThreads, kMaxThreads <= kRingSmall ? 2 : 1
 
 // Backward through the ring (a slot holds a row of x, then its row of dy); grid
 // and partial sums as in norm_backward_kernel.  (Measured on B200, 32760 x 5120
-// bf16: 160 us, 6.3 TB/s, bound by HBM; 16384 x 1536 fp16 38 us, 4.0 TB/s, of
-// which the start and the partial sums of 1036 CTAs take some 8.)
+// bf16: 160 us, 6.3 TB/s, bound by HBM; 16384 x 1536 fp16 34 us, 4.5 TB/s,
+// start and partial sums included.)
 template <typename T, int kMaxThreads>
 __global__ void __launch_bounds__(kMaxThreads, kMaxThreads <= kRingSmall ? 2 : 1)
     norm_backward_ring_kernel(const NormArgs p, int slots, uint32_t* err) {
@@ -1217,7 +1217,9 @@ RingShape ring_shape(int64_t K, int elem, bool vec, int rows_per_slot) {
     const int threads = static_cast<int>((K + kRingCols - 1) / kRingCols + 31) / 32 * 32;
     if (!vec || threads <= 32 || threads > kRingLarge) return {0, 0, 0, 0};
     const int64_t slot = K * elem * rows_per_slot;
-    const int per_sm = std::min(8, std::max(1, 21 / (threads / 32)));  // at 96 registers 21 warps fit
+    // At 96 registers five warps fit each of the SM's four schedulers.  (A grid
+    // for 21 ran a second wave: 32760 x 1536 backward 71 us against 62.)
+    const int per_sm = std::min(10, std::max(1, 20 / (threads / 32)));
     // about 144 KB of rows in flight per SM
     const int slots = static_cast<int>(std::max<int64_t>(2, std::min<int64_t>(kRingMaxSlots, 144 * 1024 / (slot * per_sm))));
     return {threads, per_sm, slots, static_cast<size_t>(slot * slots)};
