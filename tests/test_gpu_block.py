@@ -8,6 +8,8 @@ the norm itself by far less (1e-4 (1 + |y|), see the norm's own tests).  The
 Linear and the rotation are checked from their actual inputs with the bounds of
 their own tests.  Everything else here is the same bits.
 """
+import threading
+
 import pytest
 import torch
 
@@ -349,3 +351,32 @@ def test_refusals_on_the_gpu():
         tfq.tfq_layer_norm(x.cpu(), w)
     with pytest.raises(ValueError):
         tfq.tfq_layer_norm(x, w.cpu())
+
+
+@pytest.mark.parametrize("M", [30, 300, 700])
+@pytest.mark.parametrize("N,K,R", [(8, 16, 8), (264, 16, 64), (8, 144, 24), (24, 48, 256)])
+def test_adapters_at_the_smallest_sizes(M, N, K, R):
+    p = lora_problem(M, N, K, R, 3, "any", True)
+    check_lora(p, tfq.tfq_scaled_fp8_linear_lora(**p))
+
+
+def test_host_threads_at_once():
+    """Calls from several host threads, a stream each."""
+    blocks = [Block(m, 1, seed=m) for m in (700, 33, 300, 1)]
+    want = [b.run() for b in blocks]
+    torch.cuda.synchronize()
+    outs = [[] for _ in blocks]
+
+    def work(b, o):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(10):
+                o.append(b.run())
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(b, o)) for b, o in zip(blocks, outs)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for w, o in zip(want, outs):
+        assert len(o) == 10 and all(torch.equal(w, got) for got in o)
