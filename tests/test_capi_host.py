@@ -315,3 +315,24 @@ def test_int8_multi_k_limit(lib):
 @pytest.mark.parametrize("entry", MULTI_ENTRIES)
 def test_multi_linear_without_gpu_fails_loudly(lib, entry):
     assert _multi(lib, entry=entry) in (_capi.TFQ_ECUDA, _capi.TFQ_EUNSUPPORTED)
+
+
+def test_the_entry_as_a_program_defines_everything_before_it_runs():
+    """`python __graft_entry__.py smoke`: whatever smoke() names exists by then (build and smoke themselves are stubs here)."""
+    import ast
+    import sys
+
+    path = os.path.join(ROOT, "__graft_entry__.py")
+    with open(path) as f:
+        tree = ast.parse(f.read())
+    functions = {n.name: n for n in tree.body if isinstance(n, ast.FunctionDef)}
+    names = sorted({n.id for n in ast.walk(functions["smoke"]) if isinstance(n, ast.Name)} & functions.keys())
+    functions["build"].body = ast.parse("pass").body
+    functions["smoke"].body = ast.parse(f"ran.append([f.__name__ for f in ({', '.join(names)},)])").body
+    ran, argv = [], sys.argv
+    try:
+        sys.argv = [path, "smoke"]
+        exec(compile(tree, path, "exec"), {"__name__": "__main__", "__file__": path, "ran": ran})
+    finally:
+        sys.argv = argv
+    assert ran == [names] and names
