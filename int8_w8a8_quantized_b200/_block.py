@@ -35,7 +35,8 @@ def _as_stream(stream, device):
         if stream.device != device:
             raise ValueError(f"the stream is on {stream.device}, the operands on {device}")
         return stream
-    return torch.cuda.ExternalStream(int(stream), device=device)
+    # 0 is the legacy default stream, as everywhere in the library (ExternalStream(0) would be some stream of torch's pool)
+    return torch.cuda.ExternalStream(int(stream), device=device) if stream else torch.cuda.default_stream(device)
 
 
 def _streamed(fn):

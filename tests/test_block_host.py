@@ -187,3 +187,12 @@ def test_only_tensors_are_operands():
                  lambda: tfq.tfq_lora_fold(x, None, x), lambda: tfq.tfq_layer_norm(x, stream=0)):
         with pytest.raises((TypeError, ValueError)):
             call()
+
+
+def test_stream_zero_is_the_default_stream(monkeypatch):
+    from int8_w8a8_quantized_b200 import _block
+
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device: ("default", device))
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device: (handle, device))
+    assert _block._as_stream(0, "cuda:1") == ("default", "cuda:1")
+    assert _block._as_stream(0x5000, "cuda:1") == (0x5000, "cuda:1")

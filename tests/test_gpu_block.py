@@ -380,3 +380,19 @@ def test_host_threads_at_once():
         t.join()
     for w, o in zip(want, outs):
         assert len(o) == 10 and all(torch.equal(w, got) for got in o)
+
+
+def test_stream_zero_is_the_default_stream():
+    """stream=0: behind the default stream's work, and in front of what it gets next."""
+    blk = Block(64, 1)
+    want = tfq.tfq_layer_norm(blk.x, blk.scale[0])
+    x = torch.zeros_like(blk.x)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(10_000_000)
+    x.copy_(blk.x)  # late
+    with torch.cuda.stream(torch.cuda.Stream()):
+        y = tfq.tfq_layer_norm(x, blk.scale[0], stream=0)
+    x.zero_()
+    got = y.clone()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
