@@ -39,6 +39,12 @@ def _as_stream(stream, device):
     return torch.cuda.ExternalStream(int(stream), device=device) if stream else torch.cuda.default_stream(device)
 
 
+def _under(stream, operand, name="x"):
+    """Makes `stream` the current one: what runs and what is allocated and freed in between belongs to it."""
+    _operand(operand, name)
+    return torch.cuda.stream(_as_stream(stream, operand.device))
+
+
 def _streamed(fn):
     """Adds the ``stream`` argument: the call and its allocations run under that stream."""
 
@@ -48,9 +54,7 @@ def _streamed(fn):
     def call(*args, stream=None, **kwargs):
         if stream is None:
             return fn(*args, **kwargs)
-        first = args[0] if args else kwargs.get(name)
-        _operand(first, name)
-        with torch.cuda.stream(_as_stream(stream, first.device)):
+        with _under(stream, args[0] if args else kwargs.get(name), name):
             return fn(*args, **kwargs)
 
     return call
@@ -420,14 +424,19 @@ def tfq_scaled_fp8_linear_lora(A_q, s_a, W_q, s_w, x, lora_A, lora_Bs, adapter, 
 def w8a8_lora_linear(x, W_q, s_w, lora_A, lora_Bs, adapter, bias=None, qmax: float = 448.0, stream=None):
     """w8a8_linear with low-rank adapters: per-token FP8 quantization of x, then
     the scaled GEMM with one adapter per row beside it."""
-    A_q, s_a = tfq_quant_act_fp8_per_token(x, qmax, stream=stream)
-    return tfq_scaled_fp8_linear_lora(A_q, s_a, W_q, s_w, x, lora_A, lora_Bs, adapter, bias=bias, stream=stream)
+    if stream is not None:
+        with _under(stream, x):
+            return w8a8_lora_linear(x, W_q, s_w, lora_A, lora_Bs, adapter, bias, qmax)
+    A_q, s_a = tfq_quant_act_fp8_per_token(x, qmax)
+    return tfq_scaled_fp8_linear_lora(A_q, s_a, W_q, s_w, x, lora_A, lora_Bs, adapter, bias=bias)
 
 
 def w8a8_norm_linear(x, norm_weight, norm_bias, W_q, s_w, bias=None, eps: float = 1e-6, weight_offset: float = 0.0,
                      qmax: float = 448.0, stream=None):
     """Layer norm (tfq_layer_norm's arguments) and the W8A8 Linear on it: the
     norm's rows go to E4M3 codes in one pass, then the scaled GEMM."""
-    A_q, s_a = tfq_layer_norm_quant_fp8(x, norm_weight, norm_bias, eps=eps, weight_offset=weight_offset, qmax=qmax,
-                                        stream=stream)
-    return tfq_scaled_fp8_linear(A_q, s_a, W_q, s_w, bias, stream=stream)
+    if stream is not None:
+        with _under(stream, x):
+            return w8a8_norm_linear(x, norm_weight, norm_bias, W_q, s_w, bias, eps, weight_offset, qmax)
+    A_q, s_a = tfq_layer_norm_quant_fp8(x, norm_weight, norm_bias, eps=eps, weight_offset=weight_offset, qmax=qmax)
+    return tfq_scaled_fp8_linear(A_q, s_a, W_q, s_w, bias)

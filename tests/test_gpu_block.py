@@ -396,3 +396,42 @@ def test_stream_zero_is_the_default_stream():
     got = y.clone()
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("call", ["lora", "norm"])
+def test_linears_keep_their_codes_on_the_stream_argument(call, monkeypatch):
+    """stream=: the codes between the two kernels are allocated and freed on that
+    stream, so that no other stream gets their memory while the GEMM still reads it."""
+    from int8_w8a8_quantized_b200 import _block
+
+    blk = Block(64, 1)
+    p, _ = blk.project()
+    name = "tfq_quant_act_fp8_per_token" if call == "lora" else "tfq_layer_norm_quant_fp8"
+    quantize, seen = getattr(_block, name), []
+
+    def spied(*args, **kwargs):
+        codes, s = quantize(*args, **kwargs)
+        seen.append((codes.data_ptr(), torch.cuda.current_stream()))
+        return codes, s
+
+    monkeypatch.setattr(_block, name, spied)
+
+    def run(stream=None):
+        if call == "lora":
+            return _block.w8a8_lora_linear(p["x"], blk.W_q, blk.s_w, blk.A, blk.Bs, blk.adapter, blk.bias, stream=stream)
+        return _block.w8a8_norm_linear(blk.x, blk.scale, blk.shift, blk.W_q, blk.s_w, blk.bias, weight_offset=1.0,
+                                       stream=stream)
+
+    want = run()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for handle in (s, s.cuda_stream):
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(10_000_000)
+        got = run(handle)
+        at, stream = seen[-1]
+        assert stream == s
+        taken = [torch.full((64, 512), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        assert at not in [t.data_ptr() for t in taken]
+        s.synchronize()
+        assert torch.equal(got, want)
