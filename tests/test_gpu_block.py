@@ -430,7 +430,7 @@ def test_linears_keep_their_codes_on_the_stream_argument(call, monkeypatch):
             torch.cuda._sleep(10_000_000)
         got = run(handle)
         at, stream = seen[-1]
-        assert stream == s
+        assert stream.cuda_stream == s.cuda_stream
         taken = [torch.full((64, 512), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
         assert at not in [t.data_ptr() for t in taken]
         s.synchronize()
