@@ -129,34 +129,42 @@ struct ShrinkItems {
 };
 
 // Fills order, segment and segments from key (all threads; count zeroed).
-// in_order: the keys of rows with an adapter increase already (requests one
-// after the other, the usual case).
+// in_order: every key is below the next one or its row has no adapter, which
+// all batches in the adapters' order meet (requests one after the other, the
+// usual case).  Warp 0 then compares each row with the last one before it that
+// has an adapter, so that rows without one in between, wherever they stand, do
+// not cut an adapter's rows apart; if the adapters turn out to decrease
+// somewhere, the rows are counted or ranked as any others.
 __device__ __forceinline__ void order_rows(ShrinkTail& s, int n_adapters, bool in_order) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t before = (1u << lane) - 1u;
     if (in_order) {
-        if (warp != 0) return;
-        int begin = 0, n = 0;
-        uint32_t last = kNoAdapter;  // the adapter of the row before
+        bool decreases = false;
+        if (warp == 0) {
+            int begin = 0, n = 0;
+            uint32_t last = kNoAdapter;  // the adapter of the last row that has one
 #pragma unroll
-        for (int c = 0; c < kShrinkRows / 32; ++c) {
-            const uint32_t key = s.key[c * 32 + lane], a = key / kShrinkRows;
-            uint32_t prev = __shfl_up_sync(0xFFFFFFFFu, a, 1);
-            if (lane == 0) prev = last;
-            const uint32_t has = __ballot_sync(0xFFFFFFFFu, a != kNoAdapter);
-            const uint32_t begins = __ballot_sync(0xFFFFFFFFu, a != kNoAdapter && a != prev);
-            const int at = begin + __popc(has & before);
-            if (a != kNoAdapter) s.order[at] = key;
-            if ((begins >> lane & 1u) != 0) s.segment[n + __popc(begins & before)] = static_cast<int16_t>(at);
-            begin += __popc(has);
-            n += __popc(begins);
-            last = __shfl_sync(0xFFFFFFFFu, a, 31);
+            for (int c = 0; c < kShrinkRows / 32; ++c) {
+                const uint32_t key = s.key[c * 32 + lane], a = key / kShrinkRows;
+                const uint32_t has = __ballot_sync(0xFFFFFFFFu, a != kNoAdapter);
+                const uint32_t earlier = __shfl_sync(0xFFFFFFFFu, a, 31 - __clz(static_cast<int>(has & before | 1u)));
+                const uint32_t prev = (has & before) != 0 ? earlier : last;
+                const uint32_t begins = __ballot_sync(0xFFFFFFFFu, a != kNoAdapter && a != prev);
+                decreases = decreases || (a != kNoAdapter && prev != kNoAdapter && a < prev);
+                const int at = begin + __popc(has & before);
+                if (a != kNoAdapter) s.order[at] = key;
+                if ((begins >> lane & 1u) != 0) s.segment[n + __popc(begins & before)] = static_cast<int16_t>(at);
+                begin += __popc(has);
+                n += __popc(begins);
+                const uint32_t final = __shfl_sync(0xFFFFFFFFu, a, 31 - __clz(static_cast<int>(has | 1u)));
+                if (has != 0) last = final;
+            }
+            if (lane == 0) {
+                s.segment[n] = static_cast<int16_t>(begin);
+                s.segments = n;
+            }
         }
-        if (lane == 0) {
-            s.segment[n] = static_cast<int16_t>(begin);
-            s.segments = n;
-        }
-        return;
+        if (!__syncthreads_or(decreases)) return;
     }
     if (n_adapters <= kShrinkTable) {
         if (warp != 0) return;

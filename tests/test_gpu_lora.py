@@ -181,3 +181,56 @@ def test_a_broken_adapter_stays_with_its_own_rows(M):
     y = tfq.tfq_scaled_fp8_linear_lora(**{**p, "x": x})
     rows = torch.arange(M, device="cuda") != 7
     assert torch.equal(y[rows], clean[rows])
+
+
+def bare_rows(M, n, order):
+    """Rows without an adapter (-1) between the others': of M rows, n adapters."""
+    i = torch.arange(M, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(M + n)
+    some = torch.rand(M, generator=g, device="cuda")
+    if order == "every second":
+        idx = torch.where(i % 2 == 0, i * n // M, -1)
+    elif order == "some":
+        idx = torch.where(some < 0.9, i * n // M, -1)
+    elif order == "single":  # runs cut by single rows
+        idx = torch.where(some < 0.98, i * n // M, -1)
+    elif order == "falling":  # the adapters decrease, a bare row in front of each change
+        idx = n - 1 - i * n // M
+        idx[1:][idx[1:] != idx[:-1]] = -1
+    else:  # decreasing and increasing in turn, bare rows in front of every decrease
+        idx = torch.where(i % 4 == 3, -1, (i % 4) * (n - 1) // 2)
+    return idx.to(torch.int32)
+
+
+@pytest.mark.parametrize("order", ["every second", "some", "single", "falling", "saw"])
+@pytest.mark.parametrize("M,n,R", [(140, 1, 16), (140, 3, 64), (513, 1, 64), (700, 2, 24), (2500, 1, 8), (2500, 5, 128),
+                                   (1300, 1100, 16)])
+def test_rows_without_an_adapter_between_others(M, n, R, order):
+    p = problem(M, 264, 528, R, n, "one", True)
+    p["adapter"] = bare_rows(M, n, order)
+    check(p, tfq.tfq_scaled_fp8_linear_lora(**p))
+
+
+@pytest.mark.parametrize("order", ["every second", "some"])
+@pytest.mark.parametrize("M", [256, 9472])
+def test_rows_without_an_adapter_do_not_cut_the_others_apart(M, order):
+    """Rows without an adapter scattered among the rows of one: the call takes at most twice as long
+    as with the adapter on every row (it took 4 to 17 times as long when each of them began an item)."""
+    p = problem(M, 1024, 5120, 64, 1, "one", False)
+    whole = p["adapter"]
+
+    def us(adapter):
+        out = torch.empty((M, 1024), dtype=torch.bfloat16, device="cuda")
+        best = float("inf")
+        for _ in range(5):
+            start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            start.record()
+            for _ in range(10):
+                tfq.tfq_scaled_fp8_linear_lora(**{**p, "adapter": adapter}, out=out)
+            end.record()
+            end.synchronize()
+            best = min(best, start.elapsed_time(end) * 100)
+        return best
+
+    us(whole)  # warm
+    assert us(bare_rows(M, 1, order)) <= 2 * us(whole)
