@@ -1407,16 +1407,34 @@ tfq_status launch_layer_norm(const NormCall& c, void* y, uint8_t* q, float* s, f
                                                     dim3(sh.block), 0, stream, a));
 }
 
-// Row shares per group of the backward: enough CTAs to fill the GPU once, each
-// with rows for every slot of the CTA.
+// Row shares per group of the backward.  The CTAs run in whole waves of the GPU's
+// places: of one to four waves the number is taken whose rows per CTA, times the
+// waves, are fewest (a few CTAs more than a wave run alone behind it: 32760 x
+// 5120 in 5 groups, 300 CTAs on 296 places, took 244 us, 295 take 160).  A CTA's
+// partial sums count as kPartRows rows.
 constexpr int kNormMaxSms = 160;  // the workspace formula knows no device: more SMs add no parts
+constexpr int kNormSms = 148;     // B200: the waves are chosen for it, whatever the device has
+constexpr int kPartRows = 4;
 static int64_t backward_parts(int64_t M, int64_t K, int64_t groups, int elem, bool vec, int sm_count) {
     const NormShape s = norm_shape(K, elem, vec);
     const RingShape ring = ring_shape(K, elem, vec, 2);
     const int64_t slots = ring.threads > 0 ? 1 : s.block / s.tpr;
     const int per_sm = ring.threads > 0 ? ring.per_sm : std::max(1, std::min(8, 1024 / s.block));
-    const int64_t ctas = static_cast<int64_t>(std::min(sm_count, kNormMaxSms)) * per_sm;
-    return std::max<int64_t>(1, std::min<int64_t>((M / groups + slots - 1) / slots, (ctas + groups - 1) / groups));
+    const int64_t rows = M / groups, most = (rows + slots - 1) / slots;
+    const auto parts = [&](int sms, int waves) {
+        return std::max<int64_t>(1, std::min<int64_t>(most, static_cast<int64_t>(sms) * per_sm * waves / groups));
+    };
+    int best = 1;
+    int64_t least = INT64_MAX;
+    for (int waves = 1; waves <= 4; ++waves) {
+        const int64_t n = parts(kNormSms, waves), places = static_cast<int64_t>(kNormSms) * per_sm;
+        const int64_t cost = (groups * n + places - 1) / places * ((rows + n - 1) / n + kPartRows);
+        if (cost < least) {
+            least = cost;
+            best = waves;
+        }
+    }
+    return parts(std::min(sm_count, kNormMaxSms), best);
 }
 
 int64_t layer_norm_backward_workspace(int64_t M, int64_t K, int64_t groups) {

@@ -196,3 +196,13 @@ def test_stream_zero_is_the_default_stream(monkeypatch):
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device: (handle, device))
     assert _block._as_stream(0, "cuda:1") == ("default", "cuda:1")
     assert _block._as_stream(0x5000, "cuda:1") == (0x5000, "cuda:1")
+
+
+def test_layer_norm_backward_fills_whole_waves(lib):
+    """Groups that do not divide the GPU: no CTA beyond the last full wave.  The workspace holds
+    two fp32 rows for each CTA of a device of 160 SMs; 5120 columns run two CTAs per SM at most, 1536
+    columns six."""
+    f = lib.tfq_layer_norm_backward_workspace_bytes
+    for M, K, G, per_sm in ((32760, 5120, 3, 2), (32760, 5120, 5, 2), (32760, 5120, 7, 2), (32767, 1536, 7, 6)):
+        ctas = f(M, K, G) // (2 * K * 4)
+        assert ctas % G == 0 and 0.95 * 160 * per_sm <= ctas <= 160 * per_sm
