@@ -169,7 +169,7 @@ tfq_status tfq_rope_axes(const void* q, int64_t q_row_stride, int64_t q_head_str
     DeviceState* ds = current_device_state(&st);
     if (ds == nullptr) return st;
     return launch_rope(tq, tk, M, D, dtype, positions, pos_is_64 != 0, pos_row_stride, pos_axis_stride, n_pairs,
-                       inv_freq, axis, pairing == TFQ_ROPE_HALVES, inverse != 0, static_cast<cudaStream_t>(stream));
+                       inv_freq, axis, pairing == TFQ_ROPE_HALVES, inverse != 0, static_cast<cudaStream_t>(stream), ds);
 }
 
 tfq_status tfq_lora_fold(const void* lora_B, const float* scaling, const float* s_w, int64_t n_adapters, int64_t N,

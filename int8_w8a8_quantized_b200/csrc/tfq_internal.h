@@ -191,7 +191,7 @@ struct RopeTensor {
 };
 tfq_status launch_rope(const RopeTensor& q, const RopeTensor& k, int64_t M, int D, int dtype, const void* pos,
                        bool pos64, int64_t pos_row_stride, int64_t pos_axis_stride, int pairs, const double* inv_freq,
-                       const int32_t* axis, bool halves, bool inverse, cudaStream_t stream);
+                       const int32_t* axis, bool halves, bool inverse, cudaStream_t stream, DeviceState* ds);
 
 // Low-rank adapters (tfq_lora.cu): Bs = bf16(scaling[a] B / s_w[n]), and the
 // scaled FP8 Linear with one adapter per row beside it.

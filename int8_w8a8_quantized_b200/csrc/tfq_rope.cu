@@ -34,6 +34,8 @@ namespace tfq {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeBytes = 96 * 1024;  // heads of a CTA's tokens
+constexpr int kRopeSpread = 8;         // CTAs per SM where there are tokens for them
 
 struct RopeArgs {
     RopeTensor q, k;
@@ -220,7 +222,7 @@ bool rope_aligned(const RopeTensor& t, int e) {
 
 tfq_status launch_rope(const RopeTensor& q, const RopeTensor& k, int64_t M, int D, int dtype, const void* pos,
                        bool pos64, int64_t pos_row_stride, int64_t pos_axis_stride, int pairs, const double* inv_freq,
-                       const int32_t* axis, bool halves, bool inverse, cudaStream_t stream) {
+                       const int32_t* axis, bool halves, bool inverse, cudaStream_t stream, DeviceState* ds) {
     const int heads = q.heads + k.heads;
     const int e = dtype == TFQ_DTYPE_FP32 ? 4 : 2;
     const int V = 16 / e;
@@ -247,10 +249,20 @@ tfq_status launch_rope(const RopeTensor& q, const RopeTensor& k, int64_t M, int 
         a.inv_turn[i] = inv_freq[i] * kInvTwoPi;
         a.axis[i] = static_cast<uint8_t>(axis[i]);
     }
-    // tokens per CTA: a table entry or more for every thread, and work for every token slot
+    // Tokens per CTA: a table entry for every thread while the tokens' heads stay
+    // within kRopeBytes, work for every token slot, and few enough that every SM
+    // gets kRopeSpread CTAs.  (Measured on B200, us in a graph, by the table alone
+    // and so: 7 tokens, 18 heads of 80 fp32 5.2, 2.5; 1000 tokens, 80 heads of 32,
+    // 8 pairs 17.4, 4.5; 2000 tokens, 40 heads of 256, 8 pairs 53, 13, one pair 2252,
+    // 59; 30000 tokens, 40 heads of 128, 8 pairs 131, 101; 75600 tokens, 80 heads of
+    // 128 505 both.  One token per CTA there 558; four CTAs per SM 8.4 for 1200
+    // tokens, 32 heads of 128, eight 6.4.)
     const int slots = kRopeThreads / (a.items * a.head_lanes);
     const int table_tokens = std::max(1, kRopeThreads / std::max(1, pairs));
-    a.tokens = static_cast<int>(std::min<int64_t>(M, std::max(slots, table_tokens)));
+    const int64_t token_bytes = static_cast<int64_t>(heads) * D * e;
+    const int64_t tokens = std::max<int64_t>(slots, std::min<int64_t>(table_tokens, kRopeBytes / token_bytes));
+    const int64_t spread = static_cast<int64_t>(kRopeSpread) * ds->sm_count;
+    a.tokens = static_cast<int>(std::max<int64_t>(1, std::min(tokens, (M + spread - 1) / spread)));
     const size_t smem = static_cast<size_t>(a.tokens) * pairs * sizeof(float2);
     const int64_t blocks = (M + a.tokens - 1) / a.tokens;
     auto kernel = dtype == TFQ_DTYPE_FP32   ? rope_kernel_for<float>(vec, halves)

@@ -152,3 +152,40 @@ def test_refused_calls():
     with pytest.raises(tfq.TfqError):
         tfq.tfq_rope_axes(q[..., :8].contiguous(), None, pos, inv, axis)  # more pairs than the head has
     assert tfq.tfq_rope_axes(q[:0], None, pos[:0], inv, axis)[0].shape == (0, 2, 16)
+
+
+@pytest.mark.parametrize("M", [1, 2, 147, 593, 1183, 1185, 2369, 4737])
+@pytest.mark.parametrize("H,D,rot", [(3, 32, 4), (5, 256, 2), (1, 8, 8), (40, 64, 64)])
+def test_tokens_dealt_to_the_ctas(M, H, D, rot):
+    """Token counts around whole numbers of CTAs per SM, with few pairs and many."""
+    g = torch.Generator(device="cuda").manual_seed(M + D)
+    x = torch.randn((M, H, D), generator=g, device="cuda").bfloat16()
+    pos = torch.randint(-50, 5000, (M, 1), generator=g, device="cuda")
+    inv, axis = tfq.rope_axes_frequencies([rot])
+    for pairing in ("interleaved", "halves"):
+        out, _ = tfq.tfq_rope_axes(x, None, pos, inv, axis, pairing=pairing)
+        check(out, x, pos, inv, axis, pairing, False)
+
+
+def test_few_pairs_use_the_whole_gpu():
+    """2000 tokens, 40 heads of 256: with one pair rotated the call takes at most eight times as long as with
+    all 128 (its copied part goes by elements, the other by 16 bytes; on 8 CTAs it took over a hundred times as long)."""
+    x = torch.randn((2000, 40, 256), device="cuda").bfloat16()
+    pos = torch.arange(2000, device="cuda")[:, None]
+    out = torch.empty_like(x)
+
+    def us(rot):
+        inv, axis = tfq.rope_axes_frequencies([rot])
+        best = float("inf")
+        for _ in range(5):
+            start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            start.record()
+            for _ in range(10):
+                tfq.tfq_rope_axes(x, None, pos, inv, axis, q_out=out)
+            end.record()
+            end.synchronize()
+            best = min(best, start.elapsed_time(end) * 100)
+        return best
+
+    us(256)  # warm
+    assert us(2) <= 8 * us(256)
