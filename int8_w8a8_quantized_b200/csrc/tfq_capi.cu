@@ -101,6 +101,8 @@ DeviceState* current_device_state(tfq_status* st) {
     return ds;
 }
 
+std::mutex& state_mutex() { return g_mutex; }
+
 unsigned* take_round_counter(DeviceState* ds) {
     if (ds->round_ctrs == nullptr || ds->round_slots <= 0) return nullptr;
     std::lock_guard<std::mutex> lock(g_mutex);

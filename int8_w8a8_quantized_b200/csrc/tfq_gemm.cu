@@ -1023,15 +1023,14 @@ __global__ void wait_selftest_kernel(uint64_t limit_ns, uint32_t* err) {
 // Opt-in shared memory of the scaled GEMM kernels of one accumulator kind (once per device).
 template <int kAcc>
 tfq_status set_gemm_attributes(DeviceState* ds) {
-    if (ds->gemm_attr_set[kAcc]) return TFQ_OK;
-    cudaError_t e = cudaFuncSetAttribute(scaled_mm_kernel<kAcc>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(SMEM_BYTES));
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(scaled_mm_pair_kernel<256, kAcc>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(PairCfg<256>::kSmem));
-    if (e != cudaSuccess) return fail(TFQ_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-    ds->gemm_attr_set[kAcc] = true;
-    return TFQ_OK;
+    return once_per_device(ds->gemm_attr_set[kAcc], [] {
+        cudaError_t e = cudaFuncSetAttribute(scaled_mm_kernel<kAcc>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(SMEM_BYTES));
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(scaled_mm_pair_kernel<256, kAcc>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     static_cast<int>(PairCfg<256>::kSmem));
+        return e;
+    });
 }
 
 // The tensor maps and the Linear table of the CTA-pair kernel for n Linears
@@ -1182,15 +1181,15 @@ tfq_status launch_quant_scaled_fp8_gemm(const void* x, int64_t M, int64_t K, flo
     st = pair_linear_setup(&lin, 1, M, K, maps, a);
     if (st != TFQ_OK) return st;
     auto kernel = clamp ? scaled_mm_pair_kernel<kPBN, kAccF32, 2> : scaled_mm_pair_kernel<kPBN, kAccF32, 1>;
-    if (!ds->gemm_attr_set[5]) {
-        e = cudaFuncSetAttribute(scaled_mm_pair_kernel<kPBN, kAccF32, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(C::kSmem));
+    st = once_per_device(ds->gemm_attr_set[5], [] {
+        cudaError_t e = cudaFuncSetAttribute(scaled_mm_pair_kernel<kPBN, kAccF32, 1>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(scaled_mm_pair_kernel<kPBN, kAccF32, 2>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
-        if (e != cudaSuccess) return fail(TFQ_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-        ds->gemm_attr_set[5] = true;
-    }
+        return e;
+    });
+    if (st != TFQ_OK) return st;
     a.s_a = s_a;
     a.M = static_cast<int>(M);
     a.K = static_cast<int>(K);
@@ -1257,19 +1256,18 @@ tfq_status launch_lora_pair_gemm(const void* A, const float* s_a, const void* W,
     auto kernel = width == 64   ? scaled_mm_pair_kernel<kPBN, kAccF32, 0, 64>
                   : width == 32 ? scaled_mm_pair_kernel<kPBN, kAccF32, 0, 32>
                                 : scaled_mm_pair_kernel<kPBN, kAccF32, 0, 16>;
-    if (!ds->lora_attr_set) {
+    tfq_status st = once_per_device(ds->lora_attr_set, [] {
         cudaError_t e = cudaSuccess;
         for (auto k : {scaled_mm_pair_kernel<kPBN, kAccF32, 0, 16>, scaled_mm_pair_kernel<kPBN, kAccF32, 0, 32>,
                        scaled_mm_pair_kernel<kPBN, kAccF32, 0, 64>})
             if (e == cudaSuccess)
                 e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(C::kSmemLora));
-        if (e != cudaSuccess) return fail(TFQ_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-        ds->lora_attr_set = true;
-    }
+        return e;
+    });
+    if (st != TFQ_OK) return st;
     CUtensorMap tmA;
-    tfq_status st = encode_tensor_map_2d(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, A, K, M, K, BK, BM,
-                                         CU_TENSOR_MAP_SWIZZLE_128B);
+    st = encode_tensor_map_2d(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, A, K, M, K, BK, BM, CU_TENSOR_MAP_SWIZZLE_128B);
     if (st != TFQ_OK) return st;
     LoraPairMaps maps = {};
     GemmArgs a;

@@ -551,12 +551,11 @@ tfq_status launch_mxfp8_mm(const void* A, const uint8_t* sf_a, const void* W, co
         st = encode_tensor_map_2d(&tmY, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, out, N, M, N * 2, EPI_COLS, 32,
                                   CU_TENSOR_MAP_SWIZZLE_128B);
     if (st != TFQ_OK) return st;
-    if (!ds->gemm_attr_set[3]) {
-        const cudaError_t e = cudaFuncSetAttribute(mxfp8_mm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(MX_SMEM_BYTES));
-        if (e != cudaSuccess) return fail(TFQ_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-        ds->gemm_attr_set[3] = true;
-    }
+    st = once_per_device(ds->gemm_attr_set[3], [] {
+        return cudaFuncSetAttribute(mxfp8_mm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(MX_SMEM_BYTES));
+    });
+    if (st != TFQ_OK) return st;
     GemmArgs a;
     a.s_a = nullptr;
     a.s_w = nullptr;
@@ -593,13 +592,11 @@ tfq_status launch_mxfp8_mm(const void* A, const uint8_t* sf_a, const void* W, co
             st = encode_tensor_map_2d(&tmSB, CU_TENSOR_MAP_DATA_TYPE_UINT32, sf_w, 128, ka * mx.ra_w, 512, 128, 2,
                                       CU_TENSOR_MAP_SWIZZLE_NONE);
         if (st != TFQ_OK) return st;
-        if (!ds->gemm_attr_set[4]) {
-            const cudaError_t e = cudaFuncSetAttribute(mxfp8_mm_pair_kernel,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                       static_cast<int>(MXP_SMEM_BYTES));
-            if (e != cudaSuccess) return fail(TFQ_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-            ds->gemm_attr_set[4] = true;
-        }
+        st = once_per_device(ds->gemm_attr_set[4], [] {
+            return cudaFuncSetAttribute(mxfp8_mm_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        static_cast<int>(MXP_SMEM_BYTES));
+        });
+        if (st != TFQ_OK) return st;
         const int64_t pair_tiles = ((M + 255) / 256) * static_cast<int64_t>(a.n_tiles);
         const int clusters = static_cast<int>(std::min<int64_t>(pair_tiles, ds->sm_count / 2));
         a.round_ctr = take_round_counter(ds);

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <mutex>
 #include <utility>
 
 #include "tfq.h"
@@ -37,6 +38,7 @@ struct DeviceState {
     unsigned* round_ctrs = nullptr;
     int round_slots = 0;
     int next_round_slot = 0;
+    // Launch attributes that once_per_device() has set:
     // FP8, INT8, FP8/FP16 acc, MXFP8, MXFP8 pair, FP8 pair quantizing its activations
     bool gemm_attr_set[6] = {false, false, false, false, false, false};
     bool lora_attr_set = false;    // the CTA-pair GEMM with low-rank adapters
@@ -107,6 +109,21 @@ tfq_status launch_div_selftest(const float* a, const float* b, int64_t n, float*
 
 // Self-check of the bounded wait: a wait on a barrier that never completes.
 tfq_status launch_wait_selftest(uint64_t limit_ns, cudaStream_t stream, DeviceState* ds);
+
+// The mutex of every DeviceState's fields.
+std::mutex& state_mutex();
+
+// Sets the launch attributes that `done`, a DeviceState's flag, stands for, if no
+// call on this device has: `set` returns a cudaError_t (thread safe).
+template <typename F>
+tfq_status once_per_device(bool& done, F&& set) {
+    std::lock_guard<std::mutex> lock(state_mutex());
+    if (done) return TFQ_OK;
+    const cudaError_t e = set();
+    if (e != cudaSuccess) return fail(TFQ_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    done = true;
+    return TFQ_OK;
+}
 
 // Round-counter slot for the next GEMM launch on this device (thread safe).
 unsigned* take_round_counter(DeviceState* ds);

@@ -952,13 +952,12 @@ tfq_status launch_shrink(const LoraCall& l, const float* s_a, int64_t M, int64_t
     const int least_stages = std::max(2, a.splits > 1 ? (128 * (a.R + 4) * 4 + stage - 1) / stage : 0);
     a.stages = std::max(least_stages, std::min(kShrinkMaxStages, ((per_sm == 3 ? 75 : 112) * 1024 - rest) / stage));
     const size_t smem = static_cast<size_t>(rest) + static_cast<size_t>(a.stages) * stage;
-    if (!ds->shrink_attr_set) {
-        const cudaError_t e = cudaFuncSetAttribute(lora_shrink_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-        if (e != cudaSuccess) return fail(TFQ_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-        ds->shrink_attr_set = true;
-    }
+    tfq_status st = once_per_device(ds->shrink_attr_set, [] {
+        return cudaFuncSetAttribute(lora_shrink_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    });
+    if (st != TFQ_OK) return st;
     CUtensorMap tmX, tmA;
-    tfq_status st = encode_tensor_map_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, l.x, K, M, K * 2, 64, 128,
+    st = encode_tensor_map_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, l.x, K, M, K * 2, 64, 128,
                                          CU_TENSOR_MAP_SWIZZLE_128B);
     if (st == TFQ_OK)
         st = encode_tensor_map_2d(&tmA, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, l.A, K,
@@ -1016,11 +1015,10 @@ tfq_status launch_small_lora(const void* A_q, const float* s_a, const void* W_q,
     const int least = std::max(2, (a.Mn * 512 + stage - 1) / stage);
     a.stages = std::max(least, std::min(kSmallMaxStages, (112 * 1024 - rest) / stage));
     const size_t smem = static_cast<size_t>(rest) + static_cast<size_t>(a.stages) * stage;
-    if (!ds->small_attr_set) {
-        const cudaError_t e = cudaFuncSetAttribute(small_lora_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
-        if (e != cudaSuccess) return fail(TFQ_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-        ds->small_attr_set = true;
-    }
+    st = once_per_device(ds->small_attr_set, [] {
+        return cudaFuncSetAttribute(small_lora_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+    });
+    if (st != TFQ_OK) return st;
     CUtensorMap tmW, tmX;
     st = encode_tensor_map_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, W_q, K, N, K, BK, 128, CU_TENSOR_MAP_SWIZZLE_128B);
     if (st == TFQ_OK)

@@ -1310,13 +1310,12 @@ cudaError_t ring_attributes_of() {
     return e;
 }
 tfq_status ring_attributes(DeviceState* ds) {
-    if (ds->norm_attr_set) return TFQ_OK;
-    cudaError_t e = ring_attributes_of<float>();
-    if (e == cudaSuccess) e = ring_attributes_of<__half>();
-    if (e == cudaSuccess) e = ring_attributes_of<__nv_bfloat16>();
-    if (e != cudaSuccess) return fail(TFQ_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-    ds->norm_attr_set = true;
-    return TFQ_OK;
+    return once_per_device(ds->norm_attr_set, [] {
+        cudaError_t e = ring_attributes_of<float>();
+        if (e == cudaSuccess) e = ring_attributes_of<__half>();
+        if (e == cudaSuccess) e = ring_attributes_of<__nv_bfloat16>();
+        return e;
+    });
 }
 
 int elem_size(int dtype) { return dtype == TFQ_DTYPE_FP32 ? 4 : 2; }

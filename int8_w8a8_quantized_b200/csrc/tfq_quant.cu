@@ -369,16 +369,15 @@ tfq_status launch_staged_rows(const void* x, int64_t rows, int64_t K, float qmax
                               float* s, cudaStream_t stream, DeviceState* ds) {
     auto kernel = out_int8 ? quant_rows_staged_kernel<true, false>
                            : (clamp ? quant_rows_staged_kernel<false, true> : quant_rows_staged_kernel<false, false>);
-    if (!ds->quant_attr_set) {
-        const void* fns[3] = {reinterpret_cast<const void*>(quant_rows_staged_kernel<true, false>),
-                              reinterpret_cast<const void*>(quant_rows_staged_kernel<false, true>),
-                              reinterpret_cast<const void*>(quant_rows_staged_kernel<false, false>)};
-        for (const void* f : fns) {
-            const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kStagedSmemLimit);
-            if (e != cudaSuccess) return fail(TFQ_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-        }
-        ds->quant_attr_set = true;
-    }
+    const tfq_status st = once_per_device(ds->quant_attr_set, [] {
+        cudaError_t e = cudaSuccess;
+        for (auto f : {quant_rows_staged_kernel<true, false>, quant_rows_staged_kernel<false, true>,
+                       quant_rows_staged_kernel<false, false>})
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kStagedSmemLimit);
+        return e;
+    });
+    if (st != TFQ_OK) return st;
     const int slots = static_cast<int>(std::min<int64_t>(
         kStagedMaxSlots, std::max<int64_t>(2, TFQ_QUANT_STAGED_SLOT_BYTES / (2 * K))));
     const size_t smem = static_cast<size_t>(slots) * 2 * static_cast<size_t>(K);

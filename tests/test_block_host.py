@@ -2,6 +2,8 @@
 bad call is refused before any device work, and the frequency tables of the
 rotary positions are what their definition says."""
 import ctypes
+import os
+import subprocess
 
 import pytest
 import torch
@@ -206,3 +208,18 @@ def test_layer_norm_backward_fills_whole_waves(lib):
     for M, K, G, per_sm in ((32760, 5120, 3, 2), (32760, 5120, 5, 2), (32760, 5120, 7, 2), (32767, 1536, 7, 6)):
         ctas = f(M, K, G) // (2 * K * 4)
         assert ctas % G == 0 and 0.95 * 160 * per_sm <= ctas <= 160 * per_sm
+
+
+def test_launch_attributes_are_set_once_behind_the_mutex(tmp_path):
+    """Host threads at once (under the thread sanitizer), and no launch attribute set or looked up elsewhere."""
+    exe = tmp_path / "once"
+    cuda = os.path.join(os.path.dirname(os.path.dirname(build.nvcc_path())), "include")
+    here = os.path.dirname(os.path.abspath(__file__))
+    subprocess.run(["g++", "-std=c++17", "-O1", "-fsanitize=thread", "-pthread", "-I", build.INCLUDE, "-I", build.CSRC, "-I", cuda,
+                    os.path.join(here, "c", "once_per_device.cpp"), "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
+    for path in build.sources():
+        with open(path) as f:
+            for line in f:
+                assert "attr_set" not in line or "once_per_device(" in line, (path, line)
