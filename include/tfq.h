@@ -328,9 +328,12 @@ TFQ_API tfq_status tfq_mxfp8_linear(const void *A_q, const void *sf_a, const voi
  *            a missing bias is 0); element-aligned.
  *   y      : [M, K] dense, of `dtype`, written; may be x itself (x_stride == K).
  *   mean, rstd : [M] fp32, written, or both NULL.
- * Statistics are fp32; the variance is summed from x - mean.  NaN or inf in a
- * row makes that row of y NaN (or inf) and no other.  eps == 0 is allowed (a
- * constant row is then NaN).
+ * Statistics are fp32; the variance is summed from x - mean.  The order of a
+ * row's sums, and so the last bits of its fp32 values, goes with the kernel that
+ * M, K, groups and the alignments select: the same call gives the same bits,
+ * the same row in a call of another size may differ in them (a step of `dtype`
+ * where they decide its rounding).  NaN or inf in a row makes that row of y NaN
+ * (or inf) and no other.  eps == 0 is allowed (a constant row is then NaN).
  * M == 0 or K == 0 is a no-op.
  * Errors: TFQ_EINVAL (negative sizes, unknown types, groups < 1, M % groups != 0,
  * x_stride < K, eps negative or not finite, weight_offset not finite, a null or
@@ -442,6 +445,8 @@ TFQ_API tfq_status tfq_rope_axes(const void *q, int64_t q_row_stride, int64_t q_
  *   workspace : tfq_scaled_fp8_linear_lora_workspace_bytes(M, R) bytes of device
  *       memory, 16-byte aligned (contents before and after mean nothing; calls
  *       that overlap on the GPU need workspaces of their own).
+ * R is a multiple of 8 and the same for every adapter: adapters of lower or other
+ * ranks get rows of zeros behind their own in lora_A and zeros in lora_Bs.
  * n_adapters == 0 or R == 0 is tfq_scaled_fp8_linear (x, lora_A, lora_Bs,
  * adapter and workspace are then not read).  Sums are fp32; the rank-R
  * intermediate and lora_Bs are bf16 operands of the tensor cores.

@@ -395,7 +395,8 @@ def tfq_scaled_fp8_linear_lora(A_q, s_a, W_q, s_w, x, lora_A, lora_Bs, adapter, 
     """tfq_scaled_fp8_linear with low-rank adapters beside it: out[m] +=
     scaling[a] lora_B[a] (lora_A[a] x[m]) for a = adapter[m] (int32 [M]; outside
     [0, n): none).  x bf16 [M, K]: the activations A_q was made from; lora_A
-    bf16 [n, R, K]; lora_Bs bf16 [n, N, R] from tfq_lora_fold; R a multiple of 8."""
+    bf16 [n, R, K]; lora_Bs bf16 [n, N, R] from tfq_lora_fold; R a multiple of 8
+    (adapters of lower or unequal ranks: zeros behind their own rows of both)."""
     _codes(A_q, "A_q", None)
     dev = A_q.get_device()
     _codes(W_q, "W_q", dev)

@@ -234,3 +234,40 @@ def test_rows_without_an_adapter_do_not_cut_the_others_apart(M, order):
 
     us(whole)  # warm
     assert us(bare_rows(M, 1, order)) <= 2 * us(whole)
+
+
+@pytest.mark.parametrize("M", [20, 100, 140, 700])
+def test_zero_channels(M):
+    """All-zero weight channels (scale at its floor, so that lora_Bs is some 1e15 there) and all-zero rows: the
+    channels hold bias and adapters, the rows the bias alone."""
+    p = problem(M, 264, 272, 16, 3, "any", True)
+    g = torch.Generator(device="cuda").manual_seed(M)
+    w = (0.05 * torch.randn((264, 272), generator=g, device="cuda")).bfloat16()
+    w[::5] = 0
+    p["W_q"], p["s_w"] = tfq.tfq_quant_weight_per_channel(w)
+    assert (p["s_w"][::5] < 1e-14).all()
+    p["lora_Bs"] = tfq.tfq_lora_fold(torch.randn((3, 264, 16), generator=g, device="cuda").bfloat16(), None, p["s_w"])
+    x = p["x"].clone()
+    x[::3] = 0
+    p["x"] = x
+    p["A_q"], p["s_a"] = tfq.tfq_quant_act_fp8_per_token(x)
+    y = tfq.tfq_scaled_fp8_linear_lora(**p)
+    check(p, y)
+    assert torch.equal(y[::3], p["bias"].expand(len(range(0, M, 3)), -1))
+    bare = p["adapter"] < 0
+    assert torch.equal(y[bare][:, ::5], p["bias"][::5].expand(int(bare.sum()), -1))
+
+
+@pytest.mark.parametrize("M", [9, 300])
+def test_ranks_padded_with_zeros(M):
+    """Adapters of ranks 4, 8 and 12 as rank 16: zeros behind their own rows of both factors."""
+    p = problem(M, 264, 272, 16, 3, "any", True)
+    for a, rank in enumerate((4, 8, 12)):
+        p["lora_A"][a, rank:] = 0
+        p["lora_Bs"][a, :, rank:] = 0
+    y = tfq.tfq_scaled_fp8_linear_lora(**p)
+    check(p, y)
+    junk = {**p, "lora_Bs": p["lora_Bs"].clone()}
+    for a, rank in enumerate((4, 8, 12)):  # the first factor's zeros alone are enough
+        junk["lora_Bs"][a, :, rank:] = 7.0
+    assert torch.equal(tfq.tfq_scaled_fp8_linear_lora(**junk), y)
