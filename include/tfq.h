@@ -448,8 +448,11 @@ TFQ_API tfq_status tfq_rope_axes(const void *q, int64_t q_row_stride, int64_t q_
  * R is a multiple of 8 and the same for every adapter: adapters of lower or other
  * ranks get rows of zeros behind their own in lora_A and zeros in lora_Bs.
  * n_adapters == 0 or R == 0 is tfq_scaled_fp8_linear (x, lora_A, lora_Bs,
- * adapter and workspace are then not read).  Sums are fp32; the rank-R
- * intermediate and lora_Bs are bf16 operands of the tensor cores.
+ * adapter and workspace are then not read).  Sums are fp32.  lora_Bs is a second
+ * bf16 rounding of lora_B, and the rank-R intermediate is rounded to bf16 where
+ * K > 512 and the rows are many (M > 128, or fewer with few adapters of a high
+ * rank), to 16 bits where K <= 512; it is fp32 for few rows.  Either bf16 rounding
+ * adds to the adapters' share of out an error as large as out's own rounding.
  * M == 0 or N == 0 is a no-op.
  * Errors: those of tfq_scaled_fp8_linear; TFQ_EINVAL (n_adapters or R negative,
  * R % 8 != 0, a null pointer, x, lora_A, lora_Bs or workspace not 16-byte

@@ -372,11 +372,14 @@ struct LinearOperands {
 // tile before it (whose accumulator is the other one): they are long complete
 // when their tile begins.  The even producer leaves each stage's kind in
 // shared memory, and the MMA thread does what it says.
+//
+// kHalves: t has 16 bits, as an upper and a lower bf16 half, and every chunk of it
+// is two stages, one for each half, with the same B.
 struct LoraPairMaps : PairMaps {
     CUtensorMap bs;   // Bs [n_adapters * N, R], kLora x PBN / 2 boxes
     CUtensorMap bsq;  // ... kLora x PBN / 4 boxes (half-width tiles)
     const int32_t* idx;
-    const uint4* t;  // [M, R] bf16
+    const uint4* t;  // [M, R] bf16; kHalves: [M, 2 R], upper and lower halves
     int n_adapters;
     int R;
 };
@@ -436,7 +439,7 @@ __device__ __forceinline__ bool lora_work_item(const GemmArgs& p, int w, int n_c
 }
 
 // The producer warp: the whole warp enumerates adapters, lane 0 issues.
-template <int PBN, int kWidth>
+template <int PBN, int kWidth, bool kHalves>
 struct LoraProducer {
     using C = PairCfg<PBN>;
     const CUtensorMap& tmA;
@@ -468,7 +471,8 @@ struct LoraProducer {
         const CUtensorMap* map = half < 0 ? &maps.bs : &maps.bsq;
         uint32_t a[4];
         for (int n = present.next(a, 64 / kWidth); n > 0; n = present.next(a, 64 / kWidth)) {
-            for (int c = 0; lane == 0 && c < r_chunks; ++c) {
+            for (int i = 0; lane == 0 && i < (kHalves ? 2 : 1) * r_chunks; ++i) {
+                const int c = kHalves ? i / 2 : i;
                 const int st = stage();
                 if (st < 0) break;
                 mbar_arrive(&rows_go[st]);
@@ -478,10 +482,10 @@ struct LoraProducer {
                     mbar_arrive_expect_tx(&full[st], 2 * static_cast<uint32_t>(n) * tile_bytes);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (i < n)
-                        tma_load_2d_pair(sB + st * C::kBStage + i * tile_bytes, map, c * 64,
-                                         static_cast<int>(a[i]) * p.N + b_row, full_leader, pol_b);
+                for (int j = 0; j < 4; ++j)
+                    if (j < n)
+                        tma_load_2d_pair(sB + st * C::kBStage + j * tile_bytes, map, c * 64,
+                                         static_cast<int>(a[j]) * p.N + b_row, full_leader, pol_b);
                 ++it;
             }
         }
@@ -554,7 +558,7 @@ struct LoraProducer {
 // 128 has row i of this CTA's half.  The CTA's producer tells them through
 // rows_go when such a stage is free (they skip the Linear's stages, so they
 // could not follow the phases of "empty" themselves).
-template <int PBN, int kWidth>
+template <int PBN, int kWidth, bool kHalves>
 __device__ __forceinline__ void lora_pair_rows(const LoraPairMaps& maps, const GemmArgs& p, uint8_t* sA,
                                                uint64_t* rows_go, uint64_t* rows_full,
                                                volatile int* abort_flag, int rank, int cluster, int n_clusters,
@@ -563,6 +567,7 @@ __device__ __forceinline__ void lora_pair_rows(const LoraPairMaps& maps, const G
     const int r_chunks = (maps.R + 63) / 64;
     const int units = maps.R / 8;  // 16-byte units of a row of t
     const int lead = min(kLoraLead, p.k_blocks - 1);  // as the producer
+    constexpr int kUnits = kWidth / 8;
     int it = 0;
     uint32_t phase = 0;  // a bit per stage
     int tm, tn, half;
@@ -572,51 +577,68 @@ __device__ __forceinline__ void lora_pair_rows(const LoraPairMaps& maps, const G
         const uint32_t mine = row_adapter(maps.idx, m, p.M, maps.n_adapters);
         TileAdapters present;
         present.load(maps.idx, tm, p.M, maps.n_adapters, lane);
-        uint4 v[8];
+        const uint4* t = maps.t + static_cast<int64_t>(m) * (kHalves ? 2 : 1) * units;
+        uint4 v[kUnits], low[kHalves ? kUnits : 1];
         const auto fetch = [&](int c) {
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-                v[u] = mine != 0xFFFFFFFFu && c * 8 + u < units
-                           ? __ldg(maps.t + static_cast<int64_t>(m) * units + c * 8 + u)
-                           : make_uint4(0u, 0u, 0u, 0u);
+            for (int u = 0; u < kUnits; ++u) {
+                const bool in = mine != 0xFFFFFFFFu && c * 8 + u < units;
+                v[u] = in ? __ldg(t + c * 8 + u) : make_uint4(0u, 0u, 0u, 0u);
+                if constexpr (kHalves) low[u] = in ? __ldg(t + units + c * 8 + u) : make_uint4(0u, 0u, 0u, 0u);
+            }
         };
         if (r_chunks == 1) fetch(0);
         uint32_t a[4];
+        // Waits for the next stage and stores `from` to it, masked; the stage, -1 after giving up.
+        const auto store = [&](const uint4* from, int n) {
+            const int st = it % PAIR_STAGES;
+            if (!mbar_wait_warp(&rows_go[st], (phase >> st) & 1u, abort_flag)) {
+                if (lane == 0) give_up(abort_flag, p.err, kErrLora);
+                return -1;
+            }
+            phase ^= 1u << st;
+            ++it;
+            uint8_t* dst = sA + st * C::kAStage;
+            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+            if constexpr (kWidth == 64) {  // 128-byte swizzle
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    *reinterpret_cast<uint4*>(dst + row * 128 + ((u ^ (row & 7)) << 4)) = mine == a[0] ? from[u] : zero;
+            } else if constexpr (kWidth == 32) {  // 64-byte swizzle: unit u of row r at u ^ (r / 2 % 4)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (i < n)
+                            *reinterpret_cast<uint4*>(dst + i * 8192 + row * 64 + ((u ^ ((row >> 1) & 3)) << 4)) =
+                                mine == a[i] ? from[u] : zero;
+            } else {  // 32-byte swizzle: u ^ (r / 4 % 2)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        if (i < n)
+                            *reinterpret_cast<uint4*>(dst + i * 4096 + row * 32 + ((u ^ ((row >> 2) & 1)) << 4)) =
+                                mine == a[i] ? from[u] : zero;
+            }
+            return st;
+        };
         for (int n = present.next(a, 64 / kWidth); n > 0; n = present.next(a, 64 / kWidth)) {
-            for (int c = 0; c < r_chunks; ++c, ++it) {
+            for (int c = 0; c < r_chunks; ++c) {
                 if (r_chunks > 1) fetch(c);
-                const int st = it % PAIR_STAGES;
-                if (!mbar_wait_warp(&rows_go[st], (phase >> st) & 1u, abort_flag)) {
-                    if (lane == 0) give_up(abort_flag, p.err, kErrLora);
-                    return;
-                }
-                phase ^= 1u << st;
-                uint8_t* dst = sA + st * C::kAStage;
-                const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-                if constexpr (kWidth == 64) {  // 128-byte swizzle
-#pragma unroll
-                    for (int u = 0; u < 8; ++u)
-                        *reinterpret_cast<uint4*>(dst + row * 128 + ((u ^ (row & 7)) << 4)) = mine == a[0] ? v[u] : zero;
-                } else if constexpr (kWidth == 32) {  // 64-byte swizzle: unit u of row r at u ^ (r / 2 % 4)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            if (i < n)
-                                *reinterpret_cast<uint4*>(dst + i * 8192 + row * 64 + ((u ^ ((row >> 1) & 3)) << 4)) =
-                                    mine == a[i] ? v[u] : zero;
-                } else {  // 32-byte swizzle: u ^ (r / 4 % 2)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int u = 0; u < 2; ++u)
-                            if (i < n)
-                                *reinterpret_cast<uint4*>(dst + i * 4096 + row * 32 + ((u ^ ((row >> 2) & 1)) << 4)) =
-                                    mine == a[i] ? v[u] : zero;
+                const int st = store(v, n);
+                if (st < 0) return;
+                int st2 = 0;
+                if constexpr (kHalves) {  // one fence for both halves
+                    st2 = store(low, n);
+                    if (st2 < 0) return;
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster_local_data(mapa_shared(smem_u32(&rows_full[st]), 0));
+                if (lane == 0) {
+                    mbar_arrive_cluster_local_data(mapa_shared(smem_u32(&rows_full[st]), 0));
+                    if constexpr (kHalves) mbar_arrive_cluster_local_data(mapa_shared(smem_u32(&rows_full[st2]), 0));
+                }
             }
         }
         if (w != cluster) it += lead;
@@ -747,7 +769,7 @@ struct LoraMma {
 };
 
 // kLora: 0, or the columns of an adapter's tile (16, 32 or 64).
-template <int PBN, int kAcc, int kQuant = 0, int kLora = 0>
+template <int PBN, int kAcc, int kQuant = 0, int kLora = 0, bool kHalves = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads<kQuant, kLora != 0>(), 1)
     scaled_mm_pair_kernel(const __grid_constant__ CUtensorMap tmA,
                           const __grid_constant__ std::conditional_t<kLora != 0, LoraPairMaps, PairMaps> maps,
@@ -819,10 +841,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads<kQuant,
     if (warp == 0) {
         // ---------------------------------------------------- TMA producer
         if constexpr (kLora != 0) {
-            LoraProducer<PBN, kLora> producer = {tmA,        maps,       p,
-                                          sA,         sB,         full,
-                                          empty,      rows_go,    stage_info,
-                                          abort_flag, static_cast<int>(rank), lane};
+            LoraProducer<PBN, kLora, kHalves> producer = {tmA,   maps,    p,          sA,         sB, full,
+                                                          empty, rows_go, stage_info, abort_flag,
+                                                          static_cast<int>(rank), lane};
             producer.run(cluster, n_clusters);
         } else if (lane == 0) {
             uint64_t pol_a, pol_b;
@@ -984,8 +1005,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads<kQuant,
         __syncwarp();
     } else if constexpr (kLora != 0) {
         // ------------------------------------ row warps of the adapters
-        lora_pair_rows<PBN, kLora>(maps, p, sA, rows_go, rows_full, abort_flag, static_cast<int>(rank), cluster, n_clusters,
-                            static_cast<int>(threadIdx.x) - THREADS, lane);
+        lora_pair_rows<PBN, kLora, kHalves>(maps, p, sA, rows_go, rows_full, abort_flag, static_cast<int>(rank), cluster,
+                                            n_clusters, static_cast<int>(threadIdx.x) - THREADS, lane);
     } else {
         // ------------------------------------ quantizer warps (kQuant only)
         if constexpr (kQuant != 0) quantize_rows_for_gemm<kQuant>(p, lane);
@@ -1246,20 +1267,26 @@ tfq_status launch_gemm_multi(const void* A, const float* s_a, int64_t M, int64_t
 
 }  // namespace
 
-// The Linear with the adapters' first product t [M, R] beside it.
+// The Linear with the adapters' first product t [M, R], with `halves` [M, 2 R], beside it.
 tfq_status launch_lora_pair_gemm(const void* A, const float* s_a, const void* W, const float* s_w, const void* bias,
-                                 int64_t M, int64_t N, int64_t K, const LoraCall& l, const void* t, void* out,
-                                 cudaStream_t stream, DeviceState* ds) {
+                                 int64_t M, int64_t N, int64_t K, const LoraCall& l, const void* t, bool halves,
+                                 void* out, cudaStream_t stream, DeviceState* ds) {
     constexpr int kPBN = 256;
     using C = PairCfg<kPBN>;
     const int width = l.R <= 16 ? 16 : l.R <= 32 ? 32 : 64;
     auto kernel = width == 64   ? scaled_mm_pair_kernel<kPBN, kAccF32, 0, 64>
                   : width == 32 ? scaled_mm_pair_kernel<kPBN, kAccF32, 0, 32>
                                 : scaled_mm_pair_kernel<kPBN, kAccF32, 0, 16>;
+    if (halves)
+        kernel = width == 64   ? scaled_mm_pair_kernel<kPBN, kAccF32, 0, 64, true>
+                 : width == 32 ? scaled_mm_pair_kernel<kPBN, kAccF32, 0, 32, true>
+                               : scaled_mm_pair_kernel<kPBN, kAccF32, 0, 16, true>;
     tfq_status st = once_per_device(ds->lora_attr_set, [] {
         cudaError_t e = cudaSuccess;
         for (auto k : {scaled_mm_pair_kernel<kPBN, kAccF32, 0, 16>, scaled_mm_pair_kernel<kPBN, kAccF32, 0, 32>,
-                       scaled_mm_pair_kernel<kPBN, kAccF32, 0, 64>})
+                       scaled_mm_pair_kernel<kPBN, kAccF32, 0, 64>, scaled_mm_pair_kernel<kPBN, kAccF32, 0, 16, true>,
+                       scaled_mm_pair_kernel<kPBN, kAccF32, 0, 32, true>,
+                       scaled_mm_pair_kernel<kPBN, kAccF32, 0, 64, true>})
             if (e == cudaSuccess)
                 e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(C::kSmemLora));

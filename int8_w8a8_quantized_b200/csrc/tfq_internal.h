@@ -222,10 +222,11 @@ struct LoraCall {
 };
 tfq_status launch_lora_fold(const void* B, const float* scaling, const float* s_w, int64_t n, int64_t N, int64_t R,
                             void* Bs, cudaStream_t stream);
-// (tfq_gemm.cu) the Linear on CTA pairs with t [M, R] bf16 beside it
+// (tfq_gemm.cu) the Linear on CTA pairs with t [M, R] bf16 beside it, or with
+// `halves` t [M, 2 R], the upper and lower bf16 halves of its rows
 tfq_status launch_lora_pair_gemm(const void* A, const float* s_a, const void* W, const float* s_w, const void* bias,
-                                 int64_t M, int64_t N, int64_t K, const LoraCall& l, const void* t, void* out,
-                                 cudaStream_t stream, DeviceState* ds);
+                                 int64_t M, int64_t N, int64_t K, const LoraCall& l, const void* t, bool halves,
+                                 void* out, cudaStream_t stream, DeviceState* ds);
 size_t lora_workspace_bytes(int64_t M, int64_t R);
 tfq_status launch_scaled_fp8_lora(const void* A_q, const float* s_a, const void* W_q, const float* s_w,
                                   const void* bias, int64_t M, int64_t N, int64_t K, const LoraCall& l, void* out,

@@ -41,7 +41,18 @@ __global__ void __launch_bounds__(256) lora_fold_kernel(const __nv_bfloat16* B, 
 
 // ---------------------------------------------------------------------------
 // First product, many rows (lora_shrink_kernel):
-//   t[m, r] = bf16(sum_k x[m,k] A[idx[m],r,k] / s_a[m]).
+//   t[m, r] = sum_k x[m,k] A[idx[m],r,k] / s_a[m],
+// rounded to bf16, an operand of the tensor cores, or up to K = kHalvesK left as
+// two of them, hi = bf16(t) and lo = bf16(t - hi).  (One bf16 puts an error of half
+// a step, at random, on the adapters' share of a result that is itself rounded to
+// bf16, and lora_Bs' own rounding as much again.  The Linear's sum grows with
+// sqrt(K), the adapters' does not: measured with 64-bit sums, unit weights of
+// 0.02 and adapters of 0.3, the rms error was 1.60 times that of a 32-bit form
+// at K = 64, 1.40 at 256, 1.28 at 512, 1.18 at 1024, 1.03 at 5120; with halves 1.31 at 64
+// and less above.  They cost the second product twice its stages: 20000 x 4000 x 256,
+// five adapters of rank 16 in runs, 126 us against 122; K = 64, rank 8, any order
+// 142 against 123; at 32760 x 5120 x 5120 four adapters of rank 64 in runs 3.5 %, 64
+// in any order 36 %.)
 // Rows are taken in blocks of kShrinkRows.  A CTA puts its block's rows in the
 // order of their adapters and cuts that into items of up to 128 rows of one
 // adapter, which the block's `item_ctas` CTAs share out.  An item is a
@@ -76,7 +87,7 @@ struct ShrinkArgs {
     const __nv_bfloat16* x;
     const int32_t* idx;
     const float* s_a;
-    __nv_bfloat16* t;
+    __nv_bfloat16* t;  // [M, R]; kHalves: [M, 2 R]
     uint32_t* err;
 };
 
@@ -99,6 +110,33 @@ __host__ __device__ constexpr int shrink_stage_bytes(int rn) { return kShrinkXSt
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Stores N (4 or 8) bf16 values as one access.
+template <int N>
+__device__ __forceinline__ void store_bf16(__nv_bfloat16* to, const float (&f)[N]) {
+    if constexpr (N == 8)
+        *reinterpret_cast<uint4*>(to) =
+            make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+    else
+        *reinterpret_cast<uint2*>(to) = make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3]));
+}
+
+// t of N columns from `col` on of row m: the sums f over s_a.
+template <bool kHalves, int N>
+__device__ __forceinline__ void store_t(const ShrinkArgs& p, int m, int col, float (&f)[N], float sa) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) f[j] = __fdiv_rn(f[j], sa);
+    __nv_bfloat16* t = p.t + static_cast<int64_t>(m) * (kHalves ? 2 * p.R : p.R) + col;
+    store_bf16(t, f);
+    if constexpr (kHalves) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            f[j] -= __bfloat162float(__float2bfloat16_rn(f[j]));
+            if (!isfinite(f[j])) f[j] = 0.0f;  // of an infinity or NaN the lower half is 0
+        }
+        store_bf16(t + p.R, f);
+    }
 }
 
 // The items of a block that are this CTA's: next() is false past the last.
@@ -270,7 +308,7 @@ __device__ __forceinline__ bool x_rows(ShrinkTail& s, const ShrinkArgs& p, uint8
 // Adds the S CTAs' partial sums of this CTA's share of the item's rows, in rank
 // order, and writes them to t (the epilogue's 128 threads; several remote loads
 // of each in flight).
-template <int S>
+template <int S, bool kHalves>
 __device__ __forceinline__ void join_parts(const ShrinkArgs& p, const float* part, const ShrinkItems& item, int row0,
                                            int rank) {
     constexpr int kShare = 128 / S, kBatch = S == 2 ? 4 : 1;
@@ -298,14 +336,13 @@ __device__ __forceinline__ void join_parts(const ShrinkArgs& p, const float* par
             float4 s = v[b][0];
 #pragma unroll
             for (int q = 1; q < S; ++q) s = make_float4(s.x + v[b][q].x, s.y + v[b][q].y, s.z + v[b][q].z, s.w + v[b][q].w);
-            const int m = row0 + item.row(i);
-            *reinterpret_cast<uint2*>(p.t + static_cast<int64_t>(m) * p.R + 4 * u) =
-                make_uint2(pack2(__fdiv_rn(s.x, sa[b]), __fdiv_rn(s.y, sa[b])),
-                           pack2(__fdiv_rn(s.z, sa[b]), __fdiv_rn(s.w, sa[b])));
+            float f[4] = {s.x, s.y, s.z, s.w};
+            store_t<kHalves>(p, row0 + item.row(i), 4 * u, f, sa[b]);
         }
     }
 }
 
+template <bool kHalves>
 __global__ void __launch_bounds__(kShrinkThreads, 3)
     lora_shrink_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmA,
                        const ShrinkArgs p) {
@@ -452,10 +489,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 3)
                             dst[0] = make_float4(f[0], f[1], f[2], f[3]);
                             dst[1] = make_float4(f[4], f[5], f[6], f[7]);
                         } else {
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) f[j] = __fdiv_rn(f[j], sa);
-                            *reinterpret_cast<uint4*>(p.t + static_cast<int64_t>(m) * p.R + c + 8 * h) =
-                                make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+                            store_t<kHalves>(p, m, c + 8 * h, f, sa);
                         }
                     }
                 }
@@ -470,9 +504,9 @@ __global__ void __launch_bounds__(kShrinkThreads, 3)
             __syncwarp();
             cluster_sync_all();
             if (warp >= 2) {
-                if (p.splits == 2) join_parts<2>(p, part, item, row0, rank);
-                else if (p.splits == 4) join_parts<4>(p, part, item, row0, rank);
-                else join_parts<8>(p, part, item, row0, rank);
+                if (p.splits == 2) join_parts<2, kHalves>(p, part, item, row0, rank);
+                else if (p.splits == 4) join_parts<4, kHalves>(p, part, item, row0, rank);
+                else join_parts<8, kHalves>(p, part, item, row0, rank);
             }
             __syncwarp();
             cluster_sync_after_reads();  // nobody overwrites or leaves what another still reads
@@ -913,7 +947,7 @@ cudaError_t launch_cluster(void (*kernel)(KArgs...), unsigned grid, unsigned blo
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
-tfq_status launch_shrink(const LoraCall& l, const float* s_a, int64_t M, int64_t K, __nv_bfloat16* t,
+tfq_status launch_shrink(const LoraCall& l, const float* s_a, int64_t M, int64_t K, __nv_bfloat16* t, bool halves,
                          cudaStream_t stream, DeviceState* ds) {
     ShrinkArgs a = {};
     a.M = static_cast<int>(M);
@@ -953,7 +987,10 @@ tfq_status launch_shrink(const LoraCall& l, const float* s_a, int64_t M, int64_t
     a.stages = std::max(least_stages, std::min(kShrinkMaxStages, ((per_sm == 3 ? 75 : 112) * 1024 - rest) / stage));
     const size_t smem = static_cast<size_t>(rest) + static_cast<size_t>(a.stages) * stage;
     tfq_status st = once_per_device(ds->shrink_attr_set, [] {
-        return cudaFuncSetAttribute(lora_shrink_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        cudaError_t e = cudaSuccess;
+        for (auto k : {lora_shrink_kernel<false>, lora_shrink_kernel<true>})
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        return e;
     });
     if (st != TFQ_OK) return st;
     CUtensorMap tmX, tmA;
@@ -964,8 +1001,9 @@ tfq_status launch_shrink(const LoraCall& l, const float* s_a, int64_t M, int64_t
                                   static_cast<uint64_t>(l.n_adapters) * l.R, K * 2, 64, a.Rn,
                                   CU_TENSOR_MAP_SWIZZLE_128B);
     if (st != TFQ_OK) return st;
-    return lora_launch_error(launch_cluster(lora_shrink_kernel, static_cast<unsigned>(blocks * a.item_ctas * a.splits),
-                                            kShrinkThreads, smem, a.splits, stream, tmX, tmA, a));
+    return lora_launch_error(launch_cluster(halves ? lora_shrink_kernel<true> : lora_shrink_kernel<false>,
+                                            static_cast<unsigned>(blocks * a.item_ctas * a.splits), kShrinkThreads,
+                                            smem, a.splits, stream, tmX, tmA, a));
 }
 
 }  // namespace
@@ -1040,19 +1078,20 @@ static bool use_small_lora(int64_t M, int64_t R, int64_t n_adapters) {
     return M <= kSmallM && (M * R <= 4096 || n_adapters > 8);
 }
 
-// The first product: bf16 [M, R], or fp32 for few rows.
-size_t lora_workspace_bytes(int64_t M, int64_t R) {
-    return static_cast<size_t>(M) * static_cast<size_t>(R) * (M <= kSmallM ? 4 : 2);
-}
+// The first product: fp32 for few rows, two bf16 halves up to K = kHalvesK, else
+// one (the workspace formula knows no K).
+constexpr int64_t kHalvesK = 512;
+size_t lora_workspace_bytes(int64_t M, int64_t R) { return static_cast<size_t>(M) * static_cast<size_t>(R) * 4; }
 
 tfq_status launch_scaled_fp8_lora(const void* A_q, const float* s_a, const void* W_q, const float* s_w,
                                   const void* bias, int64_t M, int64_t N, int64_t K, const LoraCall& l, void* out,
                                   cudaStream_t stream, DeviceState* ds) {
     if (use_small_lora(M, l.R, l.n_adapters)) return launch_small_lora(A_q, s_a, W_q, s_w, bias, M, N, K, l, out, stream, ds);
     __nv_bfloat16* t = static_cast<__nv_bfloat16*>(l.workspace);
-    tfq_status st = launch_shrink(l, s_a, M, K, t, stream, ds);
+    const bool halves = K <= kHalvesK;
+    tfq_status st = launch_shrink(l, s_a, M, K, t, halves, stream, ds);
     if (st != TFQ_OK) return st;
-    return launch_lora_pair_gemm(A_q, s_a, W_q, s_w, bias, M, N, K, l, t, out, stream, ds);
+    return launch_lora_pair_gemm(A_q, s_a, W_q, s_w, bias, M, N, K, l, t, halves, out, stream, ds);
 }
 
 }  // namespace tfq

@@ -271,3 +271,50 @@ def test_ranks_padded_with_zeros(M):
     for a, rank in enumerate((4, 8, 12)):  # the first factor's zeros alone are enough
         junk["lora_Bs"][a, :, rank:] = 7.0
     assert torch.equal(tfq.tfq_scaled_fp8_linear_lora(**junk), y)
+
+
+@pytest.mark.parametrize("M,K,R,order", [(40, 64, 16, "any"), (200, 64, 16, "one"), (300, 64, 8, "any"), (300, 512, 24, "any"),
+                                         (300, 64, 64, "runs"), (2500, 128, 16, "any"), (2500, 512, 72, "runs"),
+                                         (600, 64, 256, "any"), (5000, 16, 32, "any"), (40000, 48, 40, "runs")])
+def test_the_first_product_keeps_16_bits_for_a_short_sum(M, K, R, order):
+    """Adapters alone (all weight codes 0, s_w 1), K up to 512: the output is off by half a bf16 step and
+        |Bs| (2^-17 |t| + 2 K 2^-24 |x| |A| + 4 R 2^-24 |t|),
+    the lower half's rounding (2^-18) and two fp32 sums whose additions are off by a whole step at most.
+    (t in bf16 alone would be off by 2^-9 of every term.)"""
+    N, n = 264, 3
+    p = problem(M, N, K, R, n, order, False)
+    g = torch.Generator(device="cuda").manual_seed(R)
+    p["W_q"], p["s_w"] = torch.zeros_like(p["W_q"]), torch.ones_like(p["s_w"])
+    p["lora_Bs"] = torch.randn((n, N, R), generator=g, device="cuda").bfloat16()
+    y = tfq.tfq_scaled_fp8_linear_lora(**p).double()
+    tfq.tfq_device_error()
+    for a in range(-1, n):
+        rows = torch.nonzero(p["adapter"] == a).flatten()
+        if a < 0:
+            assert (y[rows] == 0).all()
+            continue
+        x, A, B = p["x"][rows].double(), p["lora_A"][a].double(), p["lora_Bs"][a].double()
+        t = x @ A.t()
+        want = t @ B.t()
+        tol = ((2.0 ** -17 + 4 * R * 2.0 ** -24) * t.abs() + 2 * K * 2.0 ** -24 * (x.abs() @ A.abs().t())) @ B.abs().t()
+        assert ((y[rows] - want).abs() <= tol + (want.abs() + tol) * 2.0 ** -8).all()
+
+
+@pytest.mark.parametrize("M,n,order", [(100, 60, "any"), (300, 3, "runs"), (2000, 3, "one"), (2000, 64, "any")])
+def test_the_error_against_a_32_bit_form(M, n, order):
+    """Adapters alone, folded: the output's rounding and that of lora_Bs have the same rms, so the error is
+    sqrt(2) times that of the products in 32 bits, rounded once (1.02: their sampling).  A bf16 t would make it
+    sqrt(3) times."""
+    N, K, R = 2000, 64, 32
+    p = problem(M, N, K, R, n, order, False)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    B = torch.randn((n, N, R), generator=g, device="cuda").bfloat16()
+    scaling = torch.rand(n, generator=g, device="cuda") + 0.5
+    p["W_q"], p["s_w"] = torch.zeros_like(p["W_q"]), torch.rand(N, generator=g, device="cuda") + 0.5
+    p["lora_Bs"] = tfq.tfq_lora_fold(B, scaling, p["s_w"])
+    want = torch.zeros((M, N), dtype=torch.float64, device="cuda")
+    for a in range(n):
+        rows = torch.nonzero(p["adapter"] == a).flatten()
+        want[rows] = (p["x"][rows].double() @ p["lora_A"][a].double().t() @ B[a].double().t()) * float(scaling[a])
+    error = lambda y: float((y.double() - want).norm())  # noqa: E731
+    assert error(tfq.tfq_scaled_fp8_linear_lora(**p)) <= 1.02 * 2 ** 0.5 * error(want.float().bfloat16())
