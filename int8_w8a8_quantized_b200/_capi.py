@@ -128,6 +128,14 @@ def _stream_handle(stream) -> int:
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _under(stream, operand):
+    """Makes `stream` the current one: buffers that a call allocates, uses on
+    `stream` and frees then belong to it, and no other stream gets their memory
+    while kernels on `stream` still use it."""
+    from . import _block
+    return _block._under(stream, operand)
+
+
 def _require(t, dtype, ndim, name, device=None):
     """Checks a tensor argument: a contiguous CUDA tensor of `dtype` (an E4M3
     code tensor may also be torch.float8_e4m3fn: the same bytes) with `ndim`
@@ -299,8 +307,11 @@ def tfq_scaled_int8_linear(A_q, s_a, W_q, s_w, bias=None, out=None, stream=None)
 
 def w8a8_int8_linear(x, W_q, s_w, bias=None, qmax: float = 127.0, stream=None):
     """The INT8 Linear: per-token INT8 quantization of x, then the scaled INT8 GEMM."""
-    A_q, s_a = tfq_quant_act_int8_per_token(x, qmax, stream=stream)
-    return tfq_scaled_int8_linear(A_q, s_a, W_q, s_w, bias, stream=stream)
+    if stream is not None:
+        with _under(stream, x):
+            return w8a8_int8_linear(x, W_q, s_w, bias, qmax)
+    A_q, s_a = tfq_quant_act_int8_per_token(x, qmax)
+    return tfq_scaled_int8_linear(A_q, s_a, W_q, s_w, bias)
 
 
 def tfq_mxfp8_scale_bytes(rows: int, K: int) -> int:
@@ -363,8 +374,11 @@ def tfq_mxfp8_linear(A_q, sf_a, W_q, sf_w, bias=None, out=None, stream=None):
 
 def mxfp8_linear(x, W_q, sf_w, bias=None, stream=None):
     """The MXFP8 Linear: block quantization of x, then the block-scaled GEMM."""
-    A_q, sf_a = tfq_quant_mxfp8(x, stream=stream)
-    return tfq_mxfp8_linear(A_q, sf_a, W_q, sf_w, bias, stream=stream)
+    if stream is not None:
+        with _under(stream, x):
+            return mxfp8_linear(x, W_q, sf_w, bias)
+    A_q, sf_a = tfq_quant_mxfp8(x)
+    return tfq_mxfp8_linear(A_q, sf_a, W_q, sf_w, bias)
 
 
 def tfq_device_error(stream=None) -> None:
@@ -374,8 +388,11 @@ def tfq_device_error(stream=None) -> None:
 
 def w8a8_linear(x, W_q, s_w, bias=None, qmax: float = 448.0, stream=None):
     """The whole Linear: per-token FP8 quantization of x, then the scaled GEMM."""
-    A_q, s_a = tfq_quant_act_fp8_per_token(x, qmax, stream=stream)
-    return tfq_scaled_fp8_linear(A_q, s_a, W_q, s_w, bias, stream=stream)
+    if stream is not None:
+        with _under(stream, x):
+            return w8a8_linear(x, W_q, s_w, bias, qmax)
+    A_q, s_a = tfq_quant_act_fp8_per_token(x, qmax)
+    return tfq_scaled_fp8_linear(A_q, s_a, W_q, s_w, bias)
 
 
 def pointer_array(ptrs):
@@ -451,6 +468,9 @@ def tfq_quant_scaled_fp8_linear(x, W_q, s_w, bias=None, qmax: float = 448.0, A_q
     quantization of x and the scaled GEMM in one call (one kernel from 512
     rows up)."""
     import torch
+    if stream is not None:
+        with _under(stream, x):
+            return tfq_quant_scaled_fp8_linear(x, W_q, s_w, bias, qmax, A_q, s_a, out, workspace)
     _require(x, torch.bfloat16, 2, "x")
     dev = x.device
     _require(W_q, torch.uint8, 2, "W_q", dev)
@@ -484,6 +504,6 @@ def tfq_quant_scaled_fp8_linear(x, W_q, s_w, bias=None, qmax: float = 448.0, A_q
         st = raw.tfq_quant_scaled_fp8_linear(x.data_ptr(), M, K, float(qmax), W_q.data_ptr(), s_w.data_ptr(),
                                              None if bias is None else bias.data_ptr(), N, A_q.data_ptr(),
                                              s_a.data_ptr(), out.data_ptr(), workspace.data_ptr(),
-                                             _stream_handle(stream))
+                                             _stream_handle(None))
     _check(st, "tfq_quant_scaled_fp8_linear")
     return out, A_q, s_a

@@ -435,3 +435,34 @@ def test_linears_keep_their_codes_on_the_stream_argument(call, monkeypatch):
         assert at not in [t.data_ptr() for t in taken]
         s.synchronize()
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("call", ["fp8", "int8", "mxfp8", "one call"])
+def test_plain_linears_keep_their_buffers_on_the_stream_argument(call, monkeypatch):
+    """The same for the Linears without adapters or norm: codes and workspaces belong to stream=."""
+    from int8_w8a8_quantized_b200 import _capi
+
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x = torch.randn((600, 512), generator=g, device="cuda").bfloat16()
+    w = torch.randn((264, 512), generator=g, device="cuda").bfloat16()
+    fp8, i8, mx = tfq.tfq_quant_weight_per_channel(w), tfq.tfq_quant_weight_per_channel(w, "int8"), tfq.tfq_quant_mxfp8(w)
+    run, kernel = {"fp8": (lambda s=None: tfq.w8a8_linear(x, *fp8, stream=s), "tfq_quant_act_fp8_per_token"),
+                   "int8": (lambda s=None: tfq.w8a8_int8_linear(x, *i8, stream=s), "tfq_quant_act_int8_per_token"),
+                   "mxfp8": (lambda s=None: tfq.mxfp8_linear(x, *mx, stream=s), "tfq_quant_mxfp8"),
+                   "one call": (lambda s=None: tfq.tfq_quant_scaled_fp8_linear(x, *fp8, stream=s)[0],
+                                "tfq_quant_scaled_fp8_linear")}[call]
+    want = run()
+    enter, seen = getattr(_capi.load_library(), kernel), []
+
+    def spied(*args):
+        seen.append((torch.cuda.current_stream().cuda_stream, args[-1]))
+        return enter(*args)
+
+    monkeypatch.setattr(_capi.raw, kernel, spied, raising=False)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream, handle in ((s, s.cuda_stream), (s.cuda_stream, s.cuda_stream), (0, 0)):
+        got = run(stream)
+        assert seen[-1] == (handle, handle)  # where the buffers are allocated, and where the kernel runs
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
