@@ -19,8 +19,10 @@
 // registers), so a large common offset costs no digits.
 //
 // Bound by HBM.  Rows of 16-byte units with 33 to 640 threads of 16 columns
-// each (K from 513 to 10240) run the ring kernels further down.  The others
-// (short rows, very long ones, rows of odd length or alignment) are read into
+// each (K from 513 to 10240) run the ring kernels further down, or, in the forward
+// and up to K = 5120, where there are rows enough, those with one or two warps
+// per row behind them.  The others (short rows, very long ones, rows of odd length
+// or alignment) are read into
 // registers: a row belongs to `tpr` threads, a power of two up to 32 (several
 // rows per warp, no barrier) or a whole CTA of up to 1024; thread t holds the
 // row's units t, t + tpr, ... (J at most).  CTAs walk consecutive rows and load
