@@ -1358,6 +1358,25 @@ int64_t norm_grid(const NormShape& s, int64_t rows, int sm_count) {
 
 }  // namespace
 
+// Row shares per group of the kernels of one or two warps per row: of one to four
+// waves of a CTA per SM the number whose turns of `at_once` rows, times the waves,
+// are fewest, a CTA's start counting as two of them.  (One wave alone, its shares
+// rounded down, left 68 SMs without work at 80 groups.  Us, that and this: 32768 x
+// 1536, 4 groups 39, 39, 50 groups 46, 45, 80 54, 45, 149 61, 54; 32768 x 5120, 80
+// groups 170, 138, 110 128, 132, 149 188, 167; to codes 80 groups 183, 140.)
+static int64_t rows_parts(int64_t rows, int64_t groups, int at_once, int sms) {
+    int64_t best = 1, least = INT64_MAX;
+    for (int waves = 1; waves <= 4; ++waves) {
+        const int64_t n = std::max<int64_t>(1, std::min<int64_t>(rows / at_once, static_cast<int64_t>(sms) * waves / groups));
+        const int64_t cost = (groups * n + sms - 1) / sms * ((rows + n * at_once - 1) / (n * at_once) + 2);
+        if (cost < least) {
+            least = cost;
+            best = n;
+        }
+    }
+    return best;
+}
+
 tfq_status launch_layer_norm(const NormCall& c, void* y, uint8_t* q, float* s, float qmax, cudaStream_t stream,
                              DeviceState* ds) {
     const int e = elem_size(c.dtype);
@@ -1381,8 +1400,7 @@ tfq_status launch_layer_norm(const NormCall& c, void* y, uint8_t* q, float* s, f
         if (rows.kernel != nullptr) {
             const tfq_status st = ring_attributes(ds);
             if (st != TFQ_OK) return st;
-            a.parts = static_cast<int>(std::max<int64_t>(
-                1, std::min<int64_t>(ds->sm_count / c.groups, c.M / c.groups / rows.rows)));
+            a.parts = static_cast<int>(rows_parts(c.M / c.groups, c.groups, rows.rows, ds->sm_count));
             return launch_error("layer norm", launch_kernel(rows.kernel, dim3(static_cast<unsigned>(a.parts * c.groups)),
                                                             dim3(32 * kRowWarps), rows.smem, stream, a, rows.slots,
                                                             ds->err_word));
