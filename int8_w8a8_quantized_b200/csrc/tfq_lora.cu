@@ -52,10 +52,10 @@ __global__ void __launch_bounds__(256) lora_fold_kernel(const __nv_bfloat16* B, 
 // sqrt(K), the adapters' does not: with weights of 0.02 and adapters whose factors
 // are 1 / sqrt(K) and 0.3 / sqrt(R), the rms error against 64 bits was 1.60 times
 // that of a 32-bit form at K = 64, 1.40 at 256, 1.28 at 512, 1.18 at 1024 and 1.04 at
-// 5120; with halves it is 1.34 at 64 and less above, all of it lora_Bs' rounding.  They cost the second product twice its stages: 20000 x 4000 x 256,
-// five adapters of rank 16 in runs, 126 us against 122; K = 64, rank 8, any order
-// 142 against 123; at 32760 x 5120 x 5120 four adapters of rank 64 in runs 3.5 %, 64
-// in any order 36 %.)
+// 5120; with halves it is 1.34 at 64 and less above, all of it lora_Bs' rounding.
+// They cost the second product twice its stages: 20000 x 4000 x 256, five adapters
+// of rank 16 in runs, 126 us against 122; K = 64, rank 8, any order 142 against 123;
+// at 32760 x 5120 x 5120 four adapters of rank 64 in runs 3.5 %, 64 in any order 36 %.)
 // Rows are taken in blocks of kShrinkRows.  A CTA puts its block's rows in the
 // order of their adapters and cuts that into items of up to 128 rows of one
 // adapter, which the block's `item_ctas` CTAs share out.  An item is a
