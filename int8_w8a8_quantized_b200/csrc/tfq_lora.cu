@@ -62,7 +62,10 @@ __global__ void __launch_bounds__(256) lora_fold_kernel(const __nv_bfloat16* B, 
 // [128, K] x [K, Rn] product on the tensor cores (Rn = R rounded up to 16):
 // its x rows come as one TMA box where they are consecutive, else row by row
 // as asynchronous copies that the epilogue's warps, idle then, issue; either
-// way every row of x is read once, and A once per item (from L2).  (Measured
+// way every row of x is used once, and A read once per item (from L2).  A box is
+// 128 rows, so a short item's brings along the rows behind it, from L2 mostly: items
+// of under 16 rows by copies instead took 144 us for 171 (64 adapters of rank 16 in any
+// order, 1777 x 5120 to 1024), but 1748 for 1583 (1000 of rank 64, 9472 rows).  (Measured
 // on B200, 12 adapters of rank 64 in any order, 9472 x 5120: streaming a
 // tile's x once for two adapters at a time and keeping each row's own product
 // 242 us, TMA gathers of four rows 116 us (some 56 cycles each), rows through
